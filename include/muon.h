@@ -323,6 +323,143 @@ MUON_API muon_status muon_profile_enable(muon_handle_t h, int enable);
  * totals.  ms and launches are HOST arrays. */
 MUON_API muon_status muon_profile_read(muon_handle_t h, double* ms, int64_t* launches);
 
+/* ------------------------------------------------------------------------------------
+ * 8-bit training operators: what stands before and after the step.  The gradient that
+ * muon_step takes is a product dW = dY^T X over a layer's saved input, and the weight it
+ * updates is an operand of the next forward pass's products.  These entry points hold
+ * both in 8 bits with one power-of-two scale per block of 128, multiply such matrices on
+ * the tensor cores' block-scaled instructions, and use the saved activations in the
+ * backward pass.
+ *
+ * Conventions beyond those at the top of this file
+ *  - A call takes a list of n independent items (n >= 0); NULL pointers are allowed where
+ *    a matrix has no element.  Rows and columns lie in 0 .. 2^24.
+ *  - Dense matrices have a row pitch `ld` (elements, >= cols), so a slice of columns of a
+ *    larger tensor can be read or written; `data` needs the alignment of its type only
+ *    (rows that are 16-byte aligned are moved faster).  Entries outside rows x cols are
+ *    left as they were.
+ *  - Written buffers must not overlap any other buffer of the call (column slices of one
+ *    tensor are told apart when they share its pitch), except where stated.
+ *  - No workspace and no allocation, after a small page-locked status word that a handle
+ *    allocates with its first call.  Calls may be captured into a CUDA graph (the first
+ *    one too), and calls on different streams may overlap on the GPU when their buffers
+ *    allow it.  Results do not depend on timing: sums run in a fixed order.
+ *  - MUON_ERR_TIMEOUT (only products wait on the device) as for muon_step, reported by
+ *    the next call or muon_sync once visible, replayed graphs included.
+ */
+
+typedef enum {
+  MUON_E4M3 = 0, /* 1-4-3, largest 448, no infinity */
+  MUON_E5M2 = 1  /* 1-5-2, largest 57344 */
+} muon_fp8_format;
+
+typedef enum {
+  MUON_BLOCK_SQUARE = 0, /* one scale per 128 x 128 block */
+  MUON_BLOCK_ROW = 1     /* one scale per 1 x 128 block (128 consecutive columns of a row) */
+} muon_fp8_blocks;
+
+/* A rows x cols matrix in 8 bits: entry (i, j) = value(codes[i*ld + j]) * 2^(byte - 127).
+ *  codes   16-byte aligned; ld a multiple of 16, >= cols
+ *  scales  the blocks' exponent bytes (255 = NaN).  SQUARE: block (i/128, j/128) at
+ *          (i/128)*ceil(cols/128) + j/128.  ROW: block (i, j/128) at (j/128)*rows + i
+ * SQUARE scales are constant along both dimensions of a block, so one copy of a matrix
+ * serves as an operand contracted over its columns (forward) and over its rows (weight
+ * and input gradients).  ROW scales follow single rows more closely and serve
+ * contractions over the columns only. */
+typedef struct {
+  void* codes;
+  void* scales;
+  int64_t rows;
+  int64_t cols;
+  int64_t ld;
+  muon_fp8_format format;
+  muon_fp8_blocks blocks;
+} muon_fp8_matrix;
+
+/* A dense row-major rows x cols matrix with row pitch ld (elements). */
+typedef struct {
+  void* data;
+  int64_t rows;
+  int64_t cols;
+  int64_t ld;
+  muon_dtype dtype;
+} muon_dense;
+
+typedef enum {
+  MUON_ACT_NONE = 0, /* f(u) = u */
+  MUON_ACT_RELU2 = 1 /* f(u) = max(u, 0)^2 (NaN stays NaN): the squared ReLU of the pages' MLPs */
+} muon_activation;
+
+/* out[i] <- f(x[i]) in 8 bits, for n matrices of equal rows and cols pairwise: a saved
+ * activation (checkpoint) of the forward pass, an operand of a product, or the 8-bit copy
+ * of a weight after a step.  f is computed in float32.  Per block, with amax the largest
+ * finite |f(x)|: e = the least integer with amax <= largest * 2^e, clamped to
+ * [-127, 127] (0 if amax = 0); codes are f(x) * 2^-e rounded to nearest-even (exact
+ * scaling, one rounding).  NaN gives NaN; an infinity gives NaN in e4m3 and an infinity in
+ * e5m2.  x and out are HOST arrays. */
+MUON_API muon_status muon_fp8_quantize(muon_handle_t h, const muon_dense* x, const muon_fp8_matrix* out, int n,
+                                       muon_activation act, void* cuda_stream);
+
+/* out[i] <- the values of x[i], rounded to nearest-even into out's dtype (exact in both
+ * dtypes except where the scaled value leaves their range): a checkpoint read back. */
+MUON_API muon_status muon_fp8_dequantize(muon_handle_t h, const muon_fp8_matrix* x, const muon_dense* out, int n,
+                                         void* cuda_stream);
+
+/* Gradient through the activation from its checkpoint alone:
+ *   du = f'(u) * dy,  RELU2: f'(u) = 2 relu(u) = 2 sqrt(h) with h = f(u) as saved,  NONE: du = dy
+ * in float32, rounded once into du[i] (dense; may be exactly dy[i]) or quantised as by
+ * muon_fp8_quantize into du8[i].  For each i one of du[i].data and du8[i].codes is given,
+ * the other is NULL; either array may be NULL altogether.  Entries of `saved` are >= 0
+ * (a negative one gives NaN). */
+MUON_API muon_status muon_fp8_act_backward(muon_handle_t h, const muon_dense* dy, const muon_fp8_matrix* saved,
+                                           const muon_dense* du, const muon_fp8_matrix* du8, int n,
+                                           muon_activation act, void* cuda_stream);
+
+typedef enum {
+  MUON_EPI_NONE = 0,
+  MUON_EPI_RELU2 = 1,         /* the result passes through f (forward: the saved activation) */
+  MUON_EPI_RELU2_BACKWARD = 2 /* the result is multiplied by 2 sqrt(saved) */
+} muon_fp8_epilogue;
+
+/* One product D = epi(C + op(A) op(B)), op(A): M x K, op(B): K x N.
+ *  a        stored M x K, or K x M with trans_a (SQUARE blocks then)
+ *  b        stored K x N (SQUARE blocks then), or N x K with trans_b
+ *  d, d8    the result: dense (d.data not NULL) or in 8 bits (d8.codes), M x N
+ *  c        optional addend (c.data not NULL): dense, M x N; may be exactly d (accumulation)
+ *  saved    M x N checkpoint, for MUON_EPI_RELU2_BACKWARD
+ * With weights W (out x in), inputs X (tokens x in) and gradients dY (tokens x out):
+ *   forward  Y = X W^T:   a = X,  b = W, trans_b
+ *   input    dX = dY W:   a = dY, b = W
+ *   weight   dW = dY^T X: a = dY, trans_a, b = X
+ * Products of codes are exact, scales are powers of two, sums are fp32 in tensor memory;
+ * the epilogue works in float32 and rounds once.  A K of 0 gives epi(C). */
+typedef struct {
+  muon_fp8_matrix a;
+  muon_fp8_matrix b;
+  int trans_a;
+  int trans_b;
+  muon_dense d;
+  muon_fp8_matrix d8;
+  muon_dense c;
+  muon_fp8_epilogue epilogue;
+  muon_fp8_matrix saved;
+} muon_fp8_product;
+
+/* n products (HOST array), independent of one another. */
+MUON_API muon_status muon_fp8_matmul(muon_handle_t h, const muon_fp8_product* products, int n, void* cuda_stream);
+
+/* Kernel kinds of the 8-bit operators, reported by muon_fp8_profile_read. */
+typedef enum {
+  MUON_FP8_KIND_QUANTIZE = 0,
+  MUON_FP8_KIND_DEQUANTIZE = 1,
+  MUON_FP8_KIND_ACT_BACKWARD = 2,
+  MUON_FP8_KIND_MATMUL = 3,
+  MUON_FP8_KIND_COUNT = 4
+} muon_fp8_kernel_kind;
+
+/* muon_profile_read for the 8-bit operators' launches (arrays of MUON_FP8_KIND_COUNT). */
+MUON_API muon_status muon_fp8_profile_read(muon_handle_t h, double* ms, int64_t* launches);
+
 /* Waits for outstanding work, frees the workspace and the handle.  Returns the
  * pending device-side status.  NULL is accepted and returns MUON_OK. */
 MUON_API muon_status muon_destroy(muon_handle_t h);

@@ -41,10 +41,21 @@ EXPORTED = ("muon_init", "muon_step", "muon_step_ex", "muon_newton_schulz", "muo
             "muon_set_launch_mode",
             "muon_workspace_bytes",
             "muon_last_launch_count", "muon_profile_enable", "muon_profile_read", "muon_destroy",
-            "muon_status_string", "muon_last_error")
+            "muon_status_string", "muon_last_error",
+            "muon_fp8_quantize", "muon_fp8_dequantize", "muon_fp8_act_backward", "muon_fp8_matmul",
+            "muon_fp8_profile_read")
 
 # muon_kernel_kind
 KERNEL_KINDS = ("momentum_norm", "gram", "poly", "update", "apply", "update_apply", "ns_persistent")
+
+# muon_fp8_kernel_kind
+FP8_KERNEL_KINDS = ("quantize", "dequantize", "act_backward", "matmul")
+
+# muon_fp8_format, muon_fp8_blocks, muon_activation, muon_fp8_epilogue
+FP8_FORMATS = {"e4m3": 0, "e5m2": 1}
+FP8_BLOCKS = {"square": 0, "row": 1}
+ACTIVATIONS = {"none": 0, "relu2": 1}
+FP8_EPILOGUES = {"none": 0, "relu2": 1, "relu2_backward": 2}
 
 # muon_launch_mode
 LAUNCH_MODES = {"auto": 0, "phases": 1, "persistent": 2}
@@ -73,6 +84,23 @@ class muon_options(ctypes.Structure):
                 ("weight_decay", ctypes.c_float), ("cautious", ctypes.c_int),
                 ("normuon", ctypes.c_int), ("normuon_beta2", ctypes.c_float), ("normuon_eps", ctypes.c_float),
                 ("normuon_state", ctypes.POINTER(ctypes.c_void_p))]
+
+
+class muon_fp8_matrix(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("ld", ctypes.c_int64), ("format", ctypes.c_int),
+                ("blocks", ctypes.c_int)]
+
+
+class muon_dense(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("ld", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
+class muon_fp8_product(ctypes.Structure):
+    _fields_ = [("a", muon_fp8_matrix), ("b", muon_fp8_matrix), ("trans_a", ctypes.c_int),
+                ("trans_b", ctypes.c_int), ("d", muon_dense), ("d8", muon_fp8_matrix), ("c", muon_dense),
+                ("epilogue", ctypes.c_int), ("saved", muon_fp8_matrix)]
 
 
 _lib_handle = None
@@ -119,6 +147,17 @@ def load_library(path: str = LIB_PATH):
     lib.muon_profile_enable.restype = i32
     lib.muon_profile_read.argtypes = [vp, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64)]
     lib.muon_profile_read.restype = i32
+    lib.muon_fp8_quantize.argtypes = [vp, ctypes.POINTER(muon_dense), ctypes.POINTER(muon_fp8_matrix), i32, i32, vp]
+    lib.muon_fp8_quantize.restype = i32
+    lib.muon_fp8_dequantize.argtypes = [vp, ctypes.POINTER(muon_fp8_matrix), ctypes.POINTER(muon_dense), i32, vp]
+    lib.muon_fp8_dequantize.restype = i32
+    lib.muon_fp8_act_backward.argtypes = [vp, ctypes.POINTER(muon_dense), ctypes.POINTER(muon_fp8_matrix),
+                                          ctypes.POINTER(muon_dense), ctypes.POINTER(muon_fp8_matrix), i32, i32, vp]
+    lib.muon_fp8_act_backward.restype = i32
+    lib.muon_fp8_matmul.argtypes = [vp, ctypes.POINTER(muon_fp8_product), i32, vp]
+    lib.muon_fp8_matmul.restype = i32
+    lib.muon_fp8_profile_read.argtypes = [vp, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64)]
+    lib.muon_fp8_profile_read.restype = i32
     lib.muon_destroy.argtypes = [vp]
     lib.muon_destroy.restype = i32
     lib.muon_status_string.argtypes = [i32]
@@ -306,6 +345,191 @@ def muon_newton_schulz_noalloc(x: torch.Tensor, out: torch.Tensor, coeffs=None, 
                                                          _stream_ptr(stream, x.device)))
 
 
+class Fp8Matrix:
+    """A rows x cols matrix in 8 bits with one power-of-two scale per block of 128 (see
+    include/muon.h): entry (i, j) = value(codes[i, j]) * 2 ** (byte - 127) with the exponent
+    byte of its block.
+
+    ``format``  "e4m3" or "e5m2"
+    ``blocks``  "square" (128 x 128; scales [row blocks, column blocks]; usable along both
+                dimensions) or "row" (1 x 128; scales [column blocks, rows])
+
+    Allocates ``codes`` (uint8, rows padded to a multiple of 16 bytes) and ``scales`` (uint8)
+    unless both are given."""
+
+    __slots__ = ("rows", "cols", "format", "blocks", "codes", "scales", "c")
+
+    def __init__(self, rows: int, cols: int, format: str = "e4m3", blocks: str = "square", device="cuda",
+                 codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None):
+        if format not in FP8_FORMATS:
+            raise ValueError(f"unknown format {format!r}; use one of {sorted(FP8_FORMATS)}")
+        if blocks not in FP8_BLOCKS:
+            raise ValueError(f"unknown blocks {blocks!r}; use one of {sorted(FP8_BLOCKS)}")
+        rows, cols = int(rows), int(cols)
+        if rows < 0 or cols < 0:
+            raise ValueError("rows and cols must be >= 0")
+        if (codes is None) != (scales is None):
+            raise ValueError("give both codes and scales, or neither")
+        bc = (cols + 127) // 128
+        shape = ((rows + 127) // 128, bc) if blocks == "square" else (bc, rows)
+        if codes is None:
+            codes = torch.empty(rows, (cols + 15) // 16 * 16, dtype=torch.uint8, device=device)
+            scales = torch.empty(shape, dtype=torch.uint8, device=device)
+        else:
+            for t, name in ((codes, "codes"), (scales, "scales")):
+                if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.uint8:
+                    raise TypeError(f"{name} must be a uint8 CUDA tensor")
+            if codes.device != scales.device:
+                raise ValueError("codes and scales must be on one device")
+            if codes.dim() != 2 or codes.shape[0] != rows or codes.shape[1] < cols:
+                raise ValueError(f"codes must hold {rows} rows of at least {cols} bytes")
+            if rows and cols and ((codes.shape[1] > 1 and codes.stride(1) != 1)
+                                  or (rows > 1 and codes.stride(0) < codes.shape[1])):
+                raise ValueError("the codes of a row must be consecutive, and rows must not overlap")
+            if tuple(scales.shape) != shape or not scales.is_contiguous():
+                raise ValueError(f"scales must be a contiguous tensor of shape {shape}")
+        self.rows, self.cols, self.format, self.blocks, self.codes, self.scales = (rows, cols, format, blocks, codes,
+                                                                                  scales)
+        # one row has no pitch of its own: any multiple of 16 that holds it will do
+        ld = codes.stride(0) if rows > 1 else (cols + 15) // 16 * 16
+        self.c = muon_fp8_matrix(codes.data_ptr(), scales.data_ptr(), rows, cols, ld, FP8_FORMATS[format],
+                                 FP8_BLOCKS[blocks])
+
+    @property
+    def shape(self):
+        return (self.rows, self.cols)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+class Fp8Product:
+    """One product out = epilogue(add + op(a) op(b)) of muon_fp8_matmul.
+
+    ``a``, ``b``    Fp8Matrix; ``trans_a`` / ``trans_b`` use them transposed
+    ``out``         CUDA tensor (bf16 / fp32, rows may be strided) or Fp8Matrix
+    ``add``         optional tensor; ``add=out`` accumulates
+    ``epilogue``    "none", "relu2", or "relu2_backward" (times 2 sqrt(``saved``))"""
+
+    __slots__ = ("a", "b", "out", "trans_a", "trans_b", "add", "epilogue", "saved")
+
+    def __init__(self, a, b, out, trans_a: bool = False, trans_b: bool = False, add=None, epilogue: str = "none",
+                 saved=None):
+        self.a, self.b, self.out, self.trans_a, self.trans_b = a, b, out, trans_a, trans_b
+        self.add, self.epilogue, self.saved = add, epilogue, saved
+
+
+def _fp8(m, name: str) -> muon_fp8_matrix:
+    if not isinstance(m, Fp8Matrix):
+        raise TypeError(f"{name} must be an Fp8Matrix")
+    return m.c
+
+
+def _dense(t: torch.Tensor, name: str) -> muon_dense:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    rows, cols = t.shape
+    if cols > 1 and rows > 0 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have consecutive columns")
+    ld = t.stride(0) if rows > 1 else cols
+    return muon_dense(t.data_ptr(), rows, cols, ld, _dtype_code(t))
+
+
+def _activation(act: str) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {act!r}; use one of {sorted(ACTIVATIONS)}")
+    return ACTIVATIONS[act]
+
+
+def _same_length(**lists) -> int:
+    lens = {len(v) for v in lists.values()}
+    if len(lens) != 1:
+        raise ValueError(f"{', '.join(lists)} must have the same length")
+    return lens.pop()
+
+
+def muon_fp8_quantize(handle, xs: Sequence[torch.Tensor], outs: Sequence[Fp8Matrix], activation: str = "none",
+                      stream=None) -> None:
+    """outs[i] <- f(xs[i]) in 8 bits (bf16 / fp32 in; f = identity or relu^2): activation
+    checkpoints, operands of products, 8-bit copies of weights."""
+    n = _same_length(xs=xs, outs=outs)
+    act = _activation(activation)
+    if n == 0:
+        return
+    x = (muon_dense * n)(*[_dense(t, "x") for t in xs])
+    o = (muon_fp8_matrix * n)(*[_fp8(m, "out") for m in outs])
+    _check(load_library().muon_fp8_quantize(handle, x, o, n, act, _stream_ptr(stream, xs[0].device)), handle)
+
+
+def muon_fp8_dequantize(handle, xs: Sequence[Fp8Matrix], outs: Sequence[torch.Tensor], stream=None) -> None:
+    """outs[i] <- the values of xs[i] (bf16 / fp32 out)."""
+    n = _same_length(xs=xs, outs=outs)
+    if n == 0:
+        return
+    x = (muon_fp8_matrix * n)(*[_fp8(m, "x") for m in xs])
+    o = (muon_dense * n)(*[_dense(t, "out") for t in outs])
+    _check(load_library().muon_fp8_dequantize(handle, x, o, n, _stream_ptr(stream, xs[0].device)), handle)
+
+
+def muon_fp8_act_backward(handle, dys: Sequence[torch.Tensor], saved: Sequence[Fp8Matrix], dus: Sequence,
+                          activation: str = "relu2", stream=None) -> None:
+    """dus[i] <- dys[i] * f'(u) from the checkpoint saved[i] = f(u); each of dus is a tensor
+    (which may be dys[i] itself) or an Fp8Matrix."""
+    n = _same_length(dys=dys, saved=saved, dus=dus)
+    act = _activation(activation)
+    if n == 0:
+        return
+    dy = (muon_dense * n)(*[_dense(t, "dy") for t in dys])
+    sv = (muon_fp8_matrix * n)(*[_fp8(m, "saved") for m in saved])
+    du, du8 = (muon_dense * n)(), (muon_fp8_matrix * n)()
+    for i, t in enumerate(dus):
+        if isinstance(t, Fp8Matrix):
+            du8[i] = t.c
+        else:
+            du[i] = _dense(t, "du")
+    _check(load_library().muon_fp8_act_backward(handle, dy, sv, du, du8, n, act, _stream_ptr(stream, dys[0].device)),
+           handle)
+
+
+def muon_fp8_matmul(handle, products: Sequence[Fp8Product], stream=None) -> None:
+    """Runs independent products out = epilogue(add + op(a) op(b)) of 8-bit matrices."""
+    n = len(products)
+    if n == 0:
+        return
+    arr = (muon_fp8_product * n)()
+    for i, p in enumerate(products):
+        q = arr[i]
+        q.a, q.b = _fp8(p.a, "a"), _fp8(p.b, "b")
+        q.trans_a, q.trans_b = (1 if p.trans_a else 0), (1 if p.trans_b else 0)
+        if isinstance(p.out, Fp8Matrix):
+            q.d8 = p.out.c
+        else:
+            q.d = _dense(p.out, "out")
+        if p.add is not None:
+            q.c = _dense(p.add, "add")
+        if p.epilogue not in FP8_EPILOGUES:
+            raise ValueError(f"unknown epilogue {p.epilogue!r}; use one of {sorted(FP8_EPILOGUES)}")
+        q.epilogue = FP8_EPILOGUES[p.epilogue]
+        if (p.saved is not None) != (p.epilogue == "relu2_backward"):
+            raise ValueError("saved belongs to the relu2_backward epilogue, which needs it")
+        if p.saved is not None:
+            q.saved = _fp8(p.saved, "saved")
+    _check(load_library().muon_fp8_matmul(handle, arr, n, _stream_ptr(stream, products[0].a.device)), handle)
+
+
+def muon_fp8_profile_read(handle) -> dict:
+    """{kind: (total_ms, launches)} of the 8-bit operators since the last read (recorded while
+    muon_profile_enable is on)."""
+    n = len(FP8_KERNEL_KINDS)
+    ms = (ctypes.c_double * n)()
+    cnt = (ctypes.c_int64 * n)()
+    _check(load_library().muon_fp8_profile_read(handle, ms, cnt), handle)
+    return {k: (float(ms[i]), int(cnt[i])) for i, k in enumerate(FP8_KERNEL_KINDS)}
+
+
 def muon_selftest_wait_timeout(handle, limit_ns: int, stream=None) -> None:
     """Enqueues the bounded-wait diagnostic (see include/muon.h); the next muon_sync
     raises MuonError with code MUON_ERR_TIMEOUT."""
@@ -374,11 +598,34 @@ class Muon:
     def __init__(self, device: int = 0):
         self.handle = muon_init(device)
 
-    def step(self, params, grads, moms, **kw):
+    def step(self, params, grads, moms, fp8_params=None, **kw):
+        """muon_step_ex; with ``fp8_params`` (list of Fp8Matrix) the updated weights are also
+        quantised into them, on the same stream, for the next forward pass's products."""
+        if fp8_params is not None:
+            if len(fp8_params) != len(params):
+                raise ValueError("fp8_params must hold one Fp8Matrix per parameter")
+            for i, (m, w) in enumerate(zip(fp8_params, params)):
+                _fp8(m, "fp8_params entry")
+                if m.shape != tuple(w.shape):
+                    raise ValueError(f"fp8_params[{i}] is {m.shape}, the parameter {tuple(w.shape)}")
         muon_step_ex(self.handle, params, grads, moms, **kw)
+        if fp8_params is not None:
+            muon_fp8_quantize(self.handle, params, fp8_params, stream=kw.get("stream"))
 
     def newton_schulz(self, xs, outs, **kw):
         muon_newton_schulz(self.handle, xs, outs, **kw)
+
+    def fp8_quantize(self, xs, outs, **kw):
+        muon_fp8_quantize(self.handle, xs, outs, **kw)
+
+    def fp8_dequantize(self, xs, outs, **kw):
+        muon_fp8_dequantize(self.handle, xs, outs, **kw)
+
+    def fp8_act_backward(self, dys, saved, dus, **kw):
+        muon_fp8_act_backward(self.handle, dys, saved, dus, **kw)
+
+    def fp8_matmul(self, products, **kw):
+        muon_fp8_matmul(self.handle, products, **kw)
 
     def close(self):
         if self.handle is not None:

@@ -1,0 +1,96 @@
+// Internal structures of the 8-bit operators, shared by their host driver (muon_fp8.cu)
+// and kernels (k_fp8_blocks.cu, k_fp8_gemm.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace muon {
+
+constexpr int kFp8Block = 128;
+
+// A dense operand of a kernel (null data: absent).
+struct F8Dense {
+  void* data;
+  int64_t ld;    // elements
+  uint8_t bf16;  // else float32
+  uint8_t vec;   // 8 consecutive entries starting at a multiple of 8 columns are 16-byte aligned
+};
+
+// An 8-bit operand (null codes: absent).  Scale byte of entry (i, j), counted in blocks
+// of 128 columns kb = j / 128: row blocks: scales[kb * s_col + i], square blocks:
+// scales[(i / 128) * s_row + kb].
+struct F8Mat {
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t ld;
+  int32_t s_row, s_col;  // square: column blocks, unused; row: unused, rows
+  uint8_t e5m2;
+  uint8_t row_blocks;
+};
+
+// ------------------------------------------------------------------ block passes
+
+enum F8Op : int { kF8Quantize = 0, kF8Dequantize = 1, kF8ActBackward = 2 };
+
+// One matrix of a pass: out (dense or 8 bits) from in and / or saved.
+struct F8Pass {
+  F8Dense in;
+  F8Mat saved;
+  F8Dense out;
+  F8Mat out8;
+  int32_t rows, cols;
+  int32_t blocks_c;     // 128-column blocks per row of blocks
+  int32_t block_begin;  // first block of this matrix inside the launch
+};
+constexpr int kMaxF8Passes = 96;
+struct F8PassParams {
+  F8Pass m[kMaxF8Passes];
+  int n;
+  int total_blocks;
+  int relu2;
+};
+static_assert(sizeof(F8PassParams) <= 32764, "parameters of the block passes must fit the kernel parameter space");
+
+cudaError_t launch_fp8_pass(int op, const F8PassParams& p, cudaStream_t st);
+
+// ------------------------------------------------------------------ products
+
+// Scales of an operand as the product walks them: byte of row r (M or N index) and
+// k-block kb at s[(by_row ? r : r / 128) * s_r + kb * s_k].
+struct F8Scales {
+  const uint8_t* s;
+  int32_t s_r, s_k;
+  int32_t by_row;
+};
+
+enum F8Epi : int { kF8EpiNone = 0, kF8EpiRelu2 = 1, kF8EpiRelu2Backward = 2 };
+
+struct F8Product {
+  F8Scales sa, sb;
+  F8Dense d, c;
+  F8Mat d8, saved;
+  int32_t m, n, k;
+  uint8_t a_mn, b_mn;      // operand stored with M / N contiguous (contraction over its rows)
+  uint8_t a_e5m2, b_e5m2;
+  int32_t epi;
+  int32_t tiles_m, tiles_n;
+  int32_t tile_begin;      // first tile inside the launch
+};
+constexpr int kMaxF8Products = 16;
+struct __align__(64) F8GemmParams {
+  CUtensorMap map_a[kMaxF8Products];
+  CUtensorMap map_b[kMaxF8Products];
+  F8Product p[kMaxF8Products];
+  int n;
+  int total_tiles;
+  int* status;
+};
+static_assert(sizeof(F8GemmParams) <= 32764, "parameters of the 8-bit products must fit the kernel parameter space");
+
+// 128 x 128 tiles, one CTA each; `split` CTAs (a cluster: 1, 2, 4 or 8) share a tile's
+// contraction and join their sums through distributed shared memory.
+cudaError_t launch_fp8_gemm_tile(const F8GemmParams& p, int split, cudaStream_t st);
+
+}  // namespace muon

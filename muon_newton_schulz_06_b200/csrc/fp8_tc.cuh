@@ -1,0 +1,100 @@
+// Tensor-core primitives of the block-scaled 8-bit products (tcgen05 kind::mxf8f6f4 with
+// scales in tensor memory), shared by the kernels of k_fp8_gemm.cu.
+//
+// The instruction multiplies A (rows x 32 codes) and B (columns x 32 codes) and scales
+// each row's and column's 32-code product by 2^(byte - 127), one byte each.  A block of
+// 128 of the format is four such steps with the same bytes.  A 32-bit word of tensor
+// memory holds four bytes per row, and the instruction descriptor picks one of them: here
+// byte q of the word is the scale of the q-th block of 128 within a group of 512 codes,
+// so scales move to tensor memory once per 512 codes.
+//
+// 128 rows of words are 512 bytes: row r at lane r % 32, word r / 32, copied from shared
+// memory as 32 lanes x 16 bytes and replicated to the four lane quadrants.
+#pragma once
+
+#include "fp8_internal.h"
+#include "tc_primitives.cuh"
+
+namespace muon {
+namespace {
+
+constexpr int kF8K = 128;        // k-block: one scale block, one 128-byte swizzle row
+constexpr int kF8Group = 4;      // k-blocks per word of scales
+constexpr uint32_t kF8SfBytes = 512;  // words of 128 rows
+
+// Instruction descriptor: D f32, UE8M0 scales; the scale bytes' index goes in per step.
+__host__ __device__ constexpr uint32_t f8_idesc(bool a_e5m2, bool b_e5m2, bool a_mn, bool b_mn, int m, int n) {
+  return ((a_e5m2 ? 1u : 0u) << 7) | ((b_e5m2 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+         ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 7) << 27);
+}
+__device__ __forceinline__ uint32_t f8_idesc_sf(uint32_t idesc, int q) {
+  return idesc | ((uint32_t)q << 4) | ((uint32_t)q << 29);
+}
+
+// Shared-memory descriptor of a block of scale words: 32 rows of 16 bytes, no swizzle,
+// 128 bytes per group of 8 rows.
+__device__ __forceinline__ uint64_t f8_sf_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(128u >> 4) << 16;
+  d |= (uint64_t)(128u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  return d;
+}
+
+__device__ __forceinline__ void f8_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                       uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// 512 bytes of scale words to 4 columns of tensor memory, in all four lane quadrants.
+__device__ __forceinline__ void f8_copy_sf(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+__device__ __forceinline__ void f8_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ void tma_load_2d_local(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
+      : "memory");
+}
+
+// Scale words of row r0 + lane + 32 j (j = 0..3) for k-blocks kb0 .. kb0 + 3; rows and
+// k-blocks out of range take 2^0 (their codes are zero).
+__device__ __forceinline__ uint4 f8_sf_words(const F8Scales& s, int r0, int rows, int kb0, int nkb, int lane) {
+  uint32_t w[4];
+  if (!s.by_row) {
+    const uint8_t* p = s.s + (int64_t)(r0 / kFp8Block) * s.s_r + (int64_t)kb0 * s.s_k;
+    uint32_t word = 0;
+#pragma unroll
+    for (int q = 0; q < kF8Group; ++q)
+      word |= (uint32_t)((r0 < rows && kb0 + q < nkb) ? p[(int64_t)q * s.s_k] : 127) << (8 * q);
+    w[0] = w[1] = w[2] = w[3] = word;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = r0 + lane + 32 * j;
+      const uint8_t* p = s.s + (int64_t)r * s.s_r + (int64_t)kb0 * s.s_k;
+      w[j] = 0;
+#pragma unroll
+      for (int q = 0; q < kF8Group; ++q)
+        w[j] |= (uint32_t)((r < rows && kb0 + q < nkb) ? p[(int64_t)q * s.s_k] : 127) << (8 * q);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+}  // namespace
+}  // namespace muon

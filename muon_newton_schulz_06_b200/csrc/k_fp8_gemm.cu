@@ -1,0 +1,364 @@
+// Block-scaled 8-bit matrix products on tcgen05 (kind::mxf8f6f4):
+//
+//   D = epi(C + sum_kb 2^(ea + eb) sum_{k in block kb} qa qb)
+//
+// with one scale exponent per block of 128 along the contraction.  Scales are powers of
+// two, so the instruction applies them itself and the sum over all blocks stays in tensor
+// memory (fp32); no partial sum passes through registers.  Either operand may be stored
+// with its contraction along rows (MN-major): weight and input gradients read the same
+// 8-bit copies as the forward pass, untransposed.
+//
+// Tile kernel: one CTA per 128 x 128 tile of D, 256 threads:
+//   warp 0   TMA producer: 3-stage ring of 128 x 128 code tiles of A and B (16 KB each)
+//   warp 1   tensor memory, MMA issue (one thread)
+//   warp 2   scale words of both operands, one set per 512 codes, two sets in flight
+//   all      epilogue: the fp32 tile goes through shared memory (the ring's space), then
+//            half a warp per row finishes 8 columns per thread, as the block passes do
+// With few tiles, a cluster of 2, 4 or 8 CTAs splits a tile's contraction: every CTA
+// leaves its partial tile in its shared memory, and each finishes 1 / split of the rows,
+// adding the partial sums in rank order through distributed shared memory.  No workspace,
+// no atomics, one launch.
+//
+// Every mbarrier wait is bounded; on expiry the kernel writes kDevTimeout to the status
+// word, lets its copies and MMAs drain, frees tensor memory and returns.
+#include "fp8_blocks.cuh"
+#include "fp8_tc.cuh"
+
+namespace muon {
+namespace {
+
+constexpr int kT = 128;  // tile rows and columns
+constexpr int kTThreads = 256;
+constexpr int kTStages = 3;
+constexpr uint32_t kTOperand = kT * kF8K;              // 16 KB
+constexpr uint32_t kTStageBytes = 2 * kTOperand;
+constexpr int kTSfSets = 2;
+constexpr uint32_t kTSfSetBytes = 2 * kF8SfBytes;      // A words, B words
+constexpr int kTPitch = kT + 4;                        // floats per staged row
+constexpr uint32_t kTRing = kTStages * kTStageBytes;
+static_assert(kT * kTPitch * 4 <= kTRing, "the staged tile reuses the ring");
+constexpr uint32_t kTSmem = kTRing + kTSfSets * kTSfSetBytes + 256 + 1024;
+constexpr uint32_t kTTmemCols = 256;  // 128 accumulator columns, 2 x 8 columns of scales
+constexpr uint32_t kTSfCol = 128;
+
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t n;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+  return n;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_cluster_f1(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// What follows the sum for 8 consecutive entries (row, col ..): addend, activation or its
+// gradient.
+__device__ __forceinline__ void f8_finish8(const F8Product& g, int row, int col, float* v) {
+  if (g.c.data != nullptr) {
+    float c[8];
+    f8_load8(g.c, row, col, g.n, c);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += c[j];
+  }
+  if (g.epi == kF8EpiRelu2) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = f8_relu2(v[j]);
+  } else if (g.epi == kF8EpiRelu2Backward) {
+    float h[8];
+    f8_decode8(f8_load_codes8(g.saved, row, col, g.n), f8_scale(*f8_scale_at(g.saved, row, col / kFp8Block)),
+               g.saved.e5m2, h);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(f8_relu2_slope(h[j]), v[j]);
+  }
+}
+
+__global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_constant__ F8GemmParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sf_smem = smem + kTRing;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sf_smem + kTSfSets * kTSfSetBytes);
+  uint64_t* empty = full + kTStages;
+  uint64_t* sf_full = empty + kTStages;
+  uint64_t* sf_empty = sf_full + kTSfSets;
+  uint64_t* done = sf_empty + kTSfSets;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* cta_max = reinterpret_cast<float*>(tmem_slot + 2);  // this CTA's block maximum
+  float* warp_max = cta_max + 1;                             // [8]
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int split = (int)cluster_size();
+  const int rank = (int)cluster_rank();
+  const int tile = blockIdx.x / split;
+  int gi = 0;
+  while (gi + 1 < p.n && p.p[gi + 1].tile_begin <= tile) ++gi;
+  const F8Product& g = p.p[gi];
+  const int local = tile - g.tile_begin;
+  const int tm = local % g.tiles_m, tn = local / g.tiles_m;
+  const int row_t = tm * kT, col_t = tn * kT;
+  const int nkb_all = (g.k + kF8K - 1) / kF8K;
+  const int per = (nkb_all + split - 1) / split;
+  const int kb_begin = min(nkb_all, rank * per), nkb = min(nkb_all, kb_begin + per) - kb_begin;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kTStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < kTSfSets; ++s) {
+      mbar_init(&sf_full[s], 1);
+      mbar_init(&sf_empty[s], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(kTTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  auto give_up = [&]() {
+    *reinterpret_cast<volatile int*>(p.status) = kDevTimeout;  // page-locked host word
+    __threadfence_system();
+    *abort_flag = 1;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const CUtensorMap* ma = &p.map_a[gi];
+      const CUtensorMap* mb = &p.map_b[gi];
+      int issued = 0;
+      bool ok = true;
+      for (int i = 0; i < nkb; ++i) {
+        const int s = i % kTStages;
+        if (!mbar_wait(&empty[s], (uint32_t)((i / kTStages) & 1) ^ 1u, abort_flag)) { ok = false; break; }
+        mbar_arrive_expect_tx(&full[s], kTStageBytes);
+        const uint32_t a_dst = smem_u32(smem + s * kTStageBytes);
+        const int k0 = (kb_begin + i) * kF8K;
+        if (g.a_mn) tma_load_2d_local(a_dst, ma, &full[s], row_t, k0);
+        else tma_load_2d_local(a_dst, ma, &full[s], k0, row_t);
+        if (g.b_mn) tma_load_2d_local(a_dst + kTOperand, mb, &full[s], col_t, k0);
+        else tma_load_2d_local(a_dst + kTOperand, mb, &full[s], k0, col_t);
+        ++issued;
+      }
+      if (!ok) give_up();
+      // every copy has landed before the ring's space is used again or the CTA exits
+      for (int i = max(0, issued - kTStages); i < issued; ++i)
+        (void)mbar_wait(&full[i % kTStages], (uint32_t)((i / kTStages) & 1), nullptr);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = f8_idesc(g.a_e5m2, g.b_e5m2, g.a_mn, g.b_mn, kT, kT);
+      const uint32_t a_step = g.a_mn ? 4096 : 32, b_step = g.b_mn ? 4096 : 32;
+      bool ok = true;
+      for (int i = 0; i < nkb; ++i) {
+        const int s = i % kTStages, q = i % kF8Group, set = (i / kF8Group) % kTSfSets;
+        const uint32_t sfa = tmem + kTSfCol + set * 8, sfb = sfa + 4;
+        if (q == 0) {
+          if (!mbar_wait(&sf_full[set], (uint32_t)((i / (kF8Group * kTSfSets)) & 1), abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t src = smem_u32(sf_smem + set * kTSfSetBytes);
+          f8_copy_sf(sfa, f8_sf_desc(src));
+          f8_copy_sf(sfb, f8_sf_desc(src + kF8SfBytes));
+        }
+        if (!mbar_wait(&full[s], (uint32_t)((i / kTStages) & 1), abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t a_addr = smem_u32(smem + s * kTStageBytes), b_addr = a_addr + kTOperand;
+        const uint32_t id = f8_idesc_sf(idesc, q);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          f8_mma(tmem, sdesc(a_addr + k * a_step, 16, 1024), sdesc(b_addr + k * b_step, 16, 1024), id, sfa, sfb,
+                 (i > 0 || k > 0) ? 1u : 0u);
+        f8_commit(&empty[s]);
+        if (q == kF8Group - 1) f8_commit(&sf_empty[set]);
+      }
+      if (!ok) give_up();
+      f8_commit(done);
+      (void)mbar_wait(done, 0, nullptr);  // every MMA and copy issued here is complete
+    }
+  } else if (warp == 2) {
+    const int groups = (nkb + kF8Group - 1) / kF8Group;
+    for (int i = 0; i < groups; ++i) {
+      const int set = i % kTSfSets;
+      int ok = 1;
+      if (lane == 0) ok = mbar_wait(&sf_empty[set], (uint32_t)((i / kTSfSets) & 1) ^ 1u, abort_flag);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) {
+        if (lane == 0) give_up();
+        break;
+      }
+      uint8_t* dst = sf_smem + set * kTSfSetBytes + lane * 16;
+      const int kb = kb_begin + i * kF8Group;
+      *reinterpret_cast<uint4*>(dst) = f8_sf_words(g.sa, row_t, g.m, kb, nkb_all, lane);
+      *reinterpret_cast<uint4*>(dst + kF8SfBytes) = f8_sf_words(g.sb, col_t, g.n, kb, nkb_all, lane);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&sf_full[set])) : "memory");
+    }
+  }
+
+  // the accumulator is final (the issuing thread waited for it) and the ring is free
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  float* stage = reinterpret_cast<float*>(smem);
+  {
+    const int quad = warp & 3, half = warp >> 2;
+    float* dst = stage + (32 * quad + lane) * kTPitch + 64 * half;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float v[32];
+      if (nkb > 0) {
+        tmem_ld32(tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(64 * half + 32 * c), v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<float4*>(dst + 32 * c + 4 * j) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  if (split > 1) cluster_sync_all();
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTTmemCols) : "memory");
+  }
+
+  // rows rank * 128/split ... of the tile; 16 threads x 8 columns per row
+  const int rows_here = kT / split;
+  const int iters = rows_here / 16;
+  const int cl = (threadIdx.x & 15) * 8;
+  const int col = col_t + cl;
+  const uint32_t stage_addr = smem_u32(stage);
+  auto fetch = [&](int rl, float* v) {  // row rl of the tile: partial sums in rank order
+    const uint32_t off = (uint32_t)(rl * kTPitch + cl) * 4;
+    if (split == 1) {
+      const float4 a = *reinterpret_cast<const float4*>(stage + rl * kTPitch + cl);
+      const float4 b = *reinterpret_cast<const float4*>(stage + rl * kTPitch + cl + 4);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    for (int r = 0; r < split; ++r) {
+      const uint32_t at = peer_addr(stage_addr + off, (uint32_t)r);
+      const float4 a = ld_cluster_f4(at), b = ld_cluster_f4(at + 16);
+      v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+      v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    }
+  };
+
+  if (g.d8.codes == nullptr) {
+    for (int i = 0; i < iters; ++i) {
+      const int rl = rank * rows_here + 16 * i + (threadIdx.x >> 4);
+      const int row = row_t + rl;
+      if (row >= g.m || col >= g.n) continue;
+      float v[8];
+      fetch(rl, v);
+      f8_finish8(g, row, col, v);
+      f8_store8(g.d, row, col, g.n, v);
+    }
+  } else {
+    const bool e5m2 = g.d8.e5m2;
+    float v[8][8];
+    float rmax[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      rmax[i] = 0.f;
+      if (i < iters) {
+        const int rl = rank * rows_here + 16 * i + (threadIdx.x >> 4);
+        const int row = row_t + rl;
+        if (row < g.m && col < g.n) {
+          fetch(rl, v[i]);
+          f8_finish8(g, row, col, v[i]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (col + j < g.n) rmax[i] = fmaxf(rmax[i], f8_finite_abs(v[i][j]));
+        }
+      }
+    }
+    float inv = 1.f;
+    if (!g.d8.row_blocks) {
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, rmax[i]);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+      if (lane == 0) warp_max[warp] = amax;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kTThreads / 32; ++w) amax = fmaxf(amax, warp_max[w]);
+      if (split > 1) {
+        if (threadIdx.x == 0) *cta_max = amax;
+        __syncwarp();
+        cluster_sync_all();
+        for (int r = 0; r < split; ++r) amax = fmaxf(amax, ld_cluster_f1(peer_addr(smem_u32(cta_max), (uint32_t)r)));
+      }
+      const int e = f8_exponent(amax, e5m2);
+      if (threadIdx.x == 0 && rank == 0) *f8_scale_at(g.d8, row_t, tn) = (uint8_t)(e + 127);
+      inv = f8_exp2(-e);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i >= iters) break;
+      const int row = row_t + rank * rows_here + 16 * i + (threadIdx.x >> 4);
+      if (g.d8.row_blocks) {
+        float amax = rmax[i];
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+        const int e = f8_exponent(amax, e5m2);
+        if (row < g.m && (threadIdx.x & 15) == 0) *f8_scale_at(g.d8, row, tn) = (uint8_t)(e + 127);
+        inv = f8_exp2(-e);
+      }
+      if (row < g.m && col < g.n) f8_store_codes8(g.d8, row, col, g.n, f8_encode8(v[i], inv, e5m2));
+    }
+  }
+  __syncwarp();
+  if (split > 1) cluster_sync_all();  // peers have read this CTA's partial tile and maximum
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_gemm_tile(const F8GemmParams& p, int split, cudaStream_t st) {
+  if (p.total_tiles == 0) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(fp8_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.total_tiles * split));
+  cfg.blockDim = dim3(kTThreads);
+  cfg.dynamicSmemBytes = kTSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fp8_tile_kernel, p);
+}
+
+}  // namespace muon

@@ -22,8 +22,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
-#include "muon.h"
-#include "muon_internal.h"
+#include "muon_handle.h"
 
 using namespace muon;
 
@@ -50,121 +49,12 @@ muon_mode fp32_form(muon_mode mode, const int64_t* rows, const int64_t* cols, in
   return mode;
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 int round8(int v) { return (v + 7) / 8 * 8; }
 
-struct GroupPlan {
-  int s = 0, L = 0, n = 0;
-  int ld_x = 0, ld_s = 0;
-  int gid_base = 0;
-  size_t off_x[2] = {0, 0};
-  size_t off_gram = 0, off_poly = 0;
-  // 3xTF32 mode: the lo parts (the arrays above hold the hi parts)
-  size_t off_xlo[2] = {0, 0};
-  size_t off_gram_lo = 0, off_poly_lo = 0;
-};
-
-struct MatPlan {
-  int group = 0, idx = 0, gid = 0;
-  int row_base = 0;  // first entry in the NorMuon row arrays (prefix of min(rows, cols))
-  int64_t rows = 0, cols = 0;
-  bool transposed = false;
-  int n_units = 0, part_base = 0, tiles_c = 0;
-};
-
-struct ChunkPlan {
-  int g_begin = 0, g_end = 0;
-  size_t off_tiles[3] = {0, 0, 0};
-  // the persistent launch's lists (symmetric products, update): every phase in one
-  // matrix priority, larger L first, so a matrix's next phase follows its previous one
-  size_t off_ptiles[2] = {0, 0};
-  int n_tiles[3] = {0, 0, 0};
-};
-
-struct Plan {
-  bool valid = false;
-  muon_mode mode = MUON_MODE_BF16;
-  std::vector<int64_t> sig;  // rows, cols pairs
-  std::vector<GroupPlan> groups;
-  std::vector<MatPlan> mats;
-  std::vector<int> mat_of_gid;  // caller index of each global (group-major) index
-  std::vector<ChunkPlan> chunks;
-  std::vector<TcTile> tiles;  // host copy of every chunk's tile lists
-  size_t off_partials = 0, off_scale = 0, off_tiles = 0, off_rowsq = 0, off_rowf = 0, off_sched = 0, bytes = 0;
-  int total_rows = 0;
-  int total_units = 0;
-  // TMA maps per group (bf16 mode): X K-major (ping/pong), X MN-major (ping/pong), Gram, Poly
-  std::vector<CUtensorMap> map_xk[2], map_xmn[2], map_gram, map_poly;
-  // output maps (32 x 32 boxes, 64-byte swizzle) for the epilogue's TMA stores
-  std::vector<CUtensorMap> map_xout[2], map_gram_out, map_poly_out;
-  // 3xTF32 mode (fp32): X K-major and MN-major, Gram, Poly; hi and lo parts
-  std::vector<CUtensorMap> t_xk[2][2], t_xmn[2][2], t_gram[2], t_poly[2];
-  // debug mode: guard bands after every workspace region (offset, region name), their
-  // offsets on the device, and the check's result words
-  std::vector<std::pair<size_t, const char*>> guards;
-  size_t off_guard_table = 0, off_guard_result = 0;
-};
-
 }  // namespace
 
-struct muon_handle {
-  int device = 0;
-  int sm_count = 148;
-  std::string err;
-  int last_launches = 0;
-  EncodeTiledFn encode = nullptr;
-  char* ws = nullptr;
-  size_t ws_bytes = 0;
-  int* dev_status = nullptr;
-  int* host_status = nullptr;
-  cudaEvent_t status_event = nullptr;
-  bool status_pending = false;
-  Plan plan;
-  TcApplyTable* apply_table = nullptr;  // host staging of the fused weight-update table
-  // TMA momentum pass of tall matrices: the tensor maps of each caller matrix and the
-  // pointers they were encoded for (grad, momentum, workspace); cleared with the plan
-  std::vector<CUtensorMap> ewmap;
-  std::vector<const void*> ewmap_key;
-  // the same for the weight-update pass (weights, final workspace X)
-  std::vector<CUtensorMap> ewmap_apply;
-  std::vector<const void*> ewmap_apply_key;
-  // per-launch timing (muon_profile_enable)
-  bool profiling = false;
-  std::vector<cudaEvent_t> ev_free;
-  struct Pending {
-    int kind;
-    cudaEvent_t a, b;
-  };
-  std::vector<Pending> ev_pending;
-  cudaEvent_t ev_open = nullptr;
-  double prof_ms[MUON_KIND_COUNT] = {};
-  int64_t prof_launches[MUON_KIND_COUNT] = {};
-  // muon_selftest_fail_next_alloc: the next workspace allocation reports failure
-  bool fail_next_alloc = false;
-  // muon_set_launch_mode
-  int launch_mode = MUON_LAUNCH_AUTO;
-  unsigned long long stall_ns = 0;  // muon_selftest_stall_persistent (next persistent launch)
-  TcPersistParams* persist = nullptr;  // host staging of the persistent launch's parameters
-  // MUON_LOG set (and not "0") at muon_init: plan summaries and errors go to stderr
-  bool log = false;
-  // MUON_DEBUG set (and not "0") at muon_init: guard bands around workspace regions,
-  // checked after every call
-  bool debug = false;
-  // MUON_NVTX set (and not "0") at muon_init: an NVTX range around every call and every
-  // kernel launch, for timeline profilers
-  bool nvtx = false;
-  // the pointer lists of the last two calls that were found to be device memory of
-  // `device` (a call with one of them is not checked again; loops often alternate
-  // between two sets of buffers)
-  std::vector<const void*> checked_ptrs[2];
-  int checked_next = 0;
-};
-
-namespace {
+namespace muon {
 
 muon_status fail(muon_handle* h, muon_status st, const char* fmt, ...) {
   if (h) {
@@ -183,6 +73,10 @@ muon_status cuda_fail(muon_handle* h, cudaError_t e, const char* what) {
   return fail(h, MUON_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+}  // namespace muon
+
+namespace {
+
 cudaEvent_t take_event(muon_handle* h) {
   if (!h->ev_free.empty()) {
     cudaEvent_t e = h->ev_free.back();
@@ -197,14 +91,21 @@ cudaEvent_t take_event(muon_handle* h) {
   return e;
 }
 
-// Brackets one launch with events on its stream while profiling is on.
-// Name of a kernel kind in the NVTX ranges (muon_kernel_kind order).
+// Name of a kernel kind in the NVTX ranges (muon_kernel_kind order, then
+// muon_fp8_kernel_kind order).
 const char* kind_name(int kind) {
-  static const char* const names[MUON_KIND_COUNT] = {"muon momentum/norm", "muon Gram",   "muon polynomial",
-                                                     "muon update",        "muon apply",  "muon update+apply",
-                                                     "muon persistent Newton-Schulz"};
-  return kind >= 0 && kind < MUON_KIND_COUNT ? names[kind] : "muon";
+  constexpr int kNames = kFp8KindBase + MUON_FP8_KIND_COUNT;
+  static const char* const names[kNames] = {"muon momentum/norm", "muon Gram",   "muon polynomial",
+                                            "muon update",        "muon apply",  "muon update+apply",
+                                            "muon persistent Newton-Schulz",
+                                            "muon fp8 quantize",  "muon fp8 dequantize",
+                                            "muon fp8 act backward", "muon fp8 matmul"};
+  return kind >= 0 && kind < kNames ? names[kind] : "muon";
 }
+
+}  // namespace
+
+namespace muon {
 
 void prof_begin(muon_handle* h, cudaStream_t st, int kind) {
   if (h->nvtx) nvtxRangePushA(kind_name(kind));
@@ -223,18 +124,9 @@ void prof_end(muon_handle* h, int kind, cudaStream_t st) {
   h->ev_open = nullptr;
 }
 
-// Restores the caller's current device on scope exit.
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = false;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-    ok = cudaSetDevice(dev) == cudaSuccess;
-  }
-  ~DeviceGuard() {
-    if (prev >= 0) cudaSetDevice(prev);
-  }
-};
+}  // namespace muon
+
+namespace {
 
 bool finite(float v) { return std::isfinite(v); }
 
@@ -1218,8 +1110,30 @@ muon_status ensure_status(muon_handle* h) {
   return MUON_OK;
 }
 
+}  // namespace
+
+namespace muon {
+
+// The 8-bit operators' status word (written by the device itself).
+static muon_status poll_fp8_status(muon_handle* h, bool wait) {
+  if (!h->fp8_status) return MUON_OK;
+  if (wait && h->fp8_pending) {
+    const cudaError_t e = cudaEventSynchronize(h->fp8_event);
+    if (e != cudaSuccess) return cuda_fail(h, e, "fp8 event");
+    h->fp8_pending = false;
+  }
+  volatile int* word = h->fp8_status;
+  if (*word != kDevOk) {
+    *word = kDevOk;
+    return fail(h, MUON_ERR_TIMEOUT, "a device-side wait of an earlier 8-bit product timed out");
+  }
+  return MUON_OK;
+}
+
 // Reports a device-side time-out of earlier work, if its status copy has landed.
 muon_status poll_status(muon_handle* h, bool wait) {
+  const muon_status s8 = poll_fp8_status(h, wait);
+  if (s8 != MUON_OK) return s8;
   if (!h->status_pending) return MUON_OK;
   cudaError_t e = wait ? cudaEventSynchronize(h->status_event) : cudaEventQuery(h->status_event);
   if (e == cudaErrorNotReady) {
@@ -1235,6 +1149,10 @@ muon_status poll_status(muon_handle* h, bool wait) {
   }
   return MUON_OK;
 }
+
+}  // namespace muon
+
+namespace {
 
 muon_status finish_call(muon_handle* h, cudaStream_t st) {
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
@@ -1566,8 +1484,12 @@ muon_status muon_profile_enable(muon_handle_t h, int enable) {
   return MUON_OK;
 }
 
-muon_status muon_profile_read(muon_handle_t h, double* ms, int64_t* launches) {
-  if (!h || !ms || !launches) return MUON_ERR_INVALID_ARG;
+}  // extern "C"
+
+namespace {
+
+// Adds the recorded launches' times to the totals (waits for their events).
+muon_status collect_timings(muon_handle* h) {
   DeviceGuard dg(h->device);
   muon_status st = MUON_OK;
   for (auto& p : h->ev_pending) {
@@ -1576,6 +1498,9 @@ muon_status muon_profile_read(muon_handle_t h, double* ms, int64_t* launches) {
     if (e == cudaSuccess) e = cudaEventElapsedTime(&t, p.a, p.b);
     if (e != cudaSuccess) {
       st = cuda_fail(h, e, "profile event");
+    } else if (p.kind >= kFp8KindBase) {
+      h->prof8_ms[p.kind - kFp8KindBase] += t;
+      h->prof8_launches[p.kind - kFp8KindBase] += 1;
     } else {
       h->prof_ms[p.kind] += t;
       h->prof_launches[p.kind] += 1;
@@ -1584,11 +1509,33 @@ muon_status muon_profile_read(muon_handle_t h, double* ms, int64_t* launches) {
     h->ev_free.push_back(p.b);
   }
   h->ev_pending.clear();
+  return st;
+}
+
+}  // namespace
+
+extern "C" {
+
+muon_status muon_profile_read(muon_handle_t h, double* ms, int64_t* launches) {
+  if (!h || !ms || !launches) return MUON_ERR_INVALID_ARG;
+  const muon_status st = collect_timings(h);
   for (int k = 0; k < MUON_KIND_COUNT; ++k) {
     ms[k] = h->prof_ms[k];
     launches[k] = h->prof_launches[k];
     h->prof_ms[k] = 0.0;
     h->prof_launches[k] = 0;
+  }
+  return st;
+}
+
+muon_status muon_fp8_profile_read(muon_handle_t h, double* ms, int64_t* launches) {
+  if (!h || !ms || !launches) return MUON_ERR_INVALID_ARG;
+  const muon_status st = collect_timings(h);
+  for (int k = 0; k < MUON_FP8_KIND_COUNT; ++k) {
+    ms[k] = h->prof8_ms[k];
+    launches[k] = h->prof8_launches[k];
+    h->prof8_ms[k] = 0.0;
+    h->prof8_launches[k] = 0;
   }
   return st;
 }
@@ -1607,6 +1554,8 @@ muon_status muon_destroy(muon_handle_t h) {
     if (h->dev_status) cudaFree(h->dev_status);
     if (h->host_status) cudaFreeHost(h->host_status);
     if (h->status_event) cudaEventDestroy(h->status_event);
+    if (h->fp8_status) cudaFreeHost(h->fp8_status);
+    if (h->fp8_event) cudaEventDestroy(h->fp8_event);
 
     for (auto& p : h->ev_pending) {
       cudaEventDestroy(p.a);

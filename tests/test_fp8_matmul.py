@@ -1,0 +1,282 @@
+"""Block-scaled 8-bit products on the GPU against the float64 oracle.
+
+Exact cases: codes are small integers and scales small powers of two, so that every partial
+sum is an integer multiple of 2^-4 below 2^19 (K <= 8192): exact in float32 in any order,
+and the result has to be equal bit for bit.
+
+Rounded cases: fp32 accumulation of n = ceil(K / 32) + 12 additions (instruction steps, the
+join of a split contraction, the addend), each within 2^-22 of the sum of magnitudes (twice a
+truncation's step, for the alignment inside an instruction), then the rounding into the
+output's type, half a step of it."""
+
+import numpy as np
+import pytest
+import torch
+
+import muon_newton_schulz_06_b200 as mb
+from oracle import fp8
+from test_fp8_blocks import codes, exps, values
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def h():
+    handle = mb.muon_init(0)
+    yield handle
+    mb.muon_destroy(handle)
+
+
+def small_ints(rows, cols, fmt, blocks, seed):
+    """Integers -2 .. 2 under scales 2^-2 .. 2^2, as an Fp8Matrix."""
+    rng = np.random.default_rng(seed)
+    vals = fp8.code_values(fmt)
+    table = np.array([int(np.flatnonzero(vals == v)[0]) for v in (-2, -1, 0, 1, 2)], dtype=np.uint8)
+    m = mb.Fp8Matrix(rows, cols, format=fmt, blocks=blocks)
+    m.codes.fill_(0x7f)                                   # padding holds NaN: it must never be read
+    m.codes[:, :cols] = torch.from_numpy(table[rng.integers(0, 5, (rows, cols))]).cuda()
+    m.scales.copy_(torch.from_numpy((127 + rng.integers(-2, 3, tuple(m.scales.shape))).astype(np.uint8)))
+    return m
+
+
+def operands(M, N, K, ta, tb, fa="e4m3", fb="e4m3", ba="square", bb="square", seed=0):
+    a = small_ints(*((K, M) if ta else (M, K)), fa, ba, seed)
+    b = small_ints(*((N, K) if tb else (K, N)), fb, bb, seed + 1)
+    va, vb = values(a), values(b)
+    return a, b, (va.T if ta else va), (vb.T if tb else vb)
+
+
+SHAPES = [(1, 1, 1), (1, 128, 128), (5, 3, 130), (64, 512, 512), (128, 128, 128), (129, 257, 1000), (300, 200, 96),
+          (257, 130, 4096), (1000, 777, 501), (16, 2048, 640), (700, 900, 33)]
+
+
+@pytest.mark.parametrize("ta,tb", [(False, True), (False, False), (True, False), (True, True)])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_exact(h, M, N, K, ta, tb):
+    a, b, va, vb = operands(M, N, K, ta, tb, seed=M + N + K)
+    d = torch.full((M, N), 7.0, device="cuda")
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, d, trans_a=ta, trans_b=tb)])
+    mb.muon_sync(h)
+    np.testing.assert_array_equal(d.double().cpu().numpy(), va @ vb)
+
+
+@pytest.mark.parametrize("fa,fb", [("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2")])
+@pytest.mark.parametrize("ba,bb", [("row", "square"), ("square", "row"), ("row", "row")])
+def test_exact_formats_and_row_blocks(h, fa, fb, ba, bb):
+    a, b, va, vb = operands(200, 333, 700, False, True, fa, fb, ba, bb, seed=4)
+    d = torch.empty(200, 333, device="cuda")
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, d, trans_b=True)])
+    np.testing.assert_array_equal(d.double().cpu().numpy(), va @ vb)
+
+
+def test_exact_many_tiles_and_long_contractions(h):
+    """Grids of more tiles than the GPU holds at once, and few tiles with a long K."""
+    for M, N, K in [(2600, 2700, 300), (4096, 2304, 768), (256, 256, 8192), (512, 384, 8100), (8192, 130, 128)]:
+        for ta, tb in [(False, True), (True, False)]:
+            a, b, va, vb = operands(M, N, K, ta, tb, seed=K)
+            d = torch.empty(M, N, device="cuda")
+            mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, d, trans_a=ta, trans_b=tb)])
+            want = torch.from_numpy(va).cuda() @ torch.from_numpy(vb).cuda()
+            assert torch.equal(d.double(), want), (M, N, K, ta)
+
+
+def test_extreme_scales(h):
+    """Scales at the ends of the byte's range multiply to ordinary numbers; a scale of 255 is
+    NaN for its block only."""
+    M, N, K = 130, 140, 256
+    a, b, _, _ = operands(M, N, K, False, True, seed=9)
+    a.scales[0, 0], b.scales[0, 0], b.scales[1, 0] = 254, 1, 1         # 2^127 * 2^-126
+    a.scales[1, 0] = 254
+    d = torch.empty(M, N, device="cuda")
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, d, trans_b=True)])
+    np.testing.assert_array_equal(d.double().cpu().numpy(), values(a) @ values(b).T)
+    a.scales[0, 1] = 255
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, d, trans_b=True)])
+    assert d[:128].isnan().all() and not d[128:].isnan().any()
+
+
+def test_nan_code_reaches_its_row_and_column_only(h):
+    M, N, K = 200, 180, 300
+    a, b, va, vb = operands(M, N, K, False, True, seed=11)
+    a.codes[150, 299] = 0x7f
+    d = torch.empty(M, N, device="cuda")
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, d, trans_b=True)])
+    nan = d.isnan()
+    assert nan[150].all() and nan.sum() == N
+    keep = [i for i in range(M) if i != 150]
+    np.testing.assert_array_equal(d.double().cpu().numpy()[keep], (va @ vb)[keep])
+
+
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("tokens", [33, 1000])
+def test_rounded_realistic(h, out, tokens):
+    rng = np.random.default_rng(5)
+    M, N, K = tokens, 520, 1100
+    x = torch.from_numpy(rng.standard_normal((M, K)) * np.exp(rng.standard_normal((1, K)))).float().cuda()
+    w = torch.from_numpy(0.02 * rng.standard_normal((N, K))).float().cuda()
+    a, b = mb.Fp8Matrix(M, K, blocks="row"), mb.Fp8Matrix(N, K)
+    mb.muon_fp8_quantize(h, [x, w], [a, b])
+    c = torch.from_numpy(rng.standard_normal((M, N))).to(DT[out]).cuda()
+    d = torch.empty(M, N, dtype=DT[out], device="cuda")
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, d, trans_b=True, add=c)])
+    want, mag = fp8.matmul(values(a), values(b).T, c.double().cpu().numpy())
+    tol = (-(-K // 32) + 12) * 2.0 ** -22 * mag + torch.finfo(DT[out]).eps / 2 * np.abs(want) * 1.01
+    assert np.all(np.abs(d.double().cpu().numpy() - want) <= tol)
+
+
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+def test_accumulates_in_place(h, out):
+    a, b, va, vb = operands(300, 250, 2000, True, False, seed=2)
+    g = torch.randint(-50, 50, (300, 250), device="cuda").to(DT[out])
+    want = torch.from_numpy(g.double().cpu().numpy() + va @ vb)
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, g, trans_a=True, add=g)])
+    assert torch.equal(g.double().cpu(), want.to(DT[out]).double())     # exact sum, one rounding
+
+
+@pytest.mark.parametrize("blocks", ["square", "row"])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (40, 70, 64), (130, 260, 500), (300, 520, 2048), (1024, 2048, 512)])
+def test_eight_bit_results_are_exact(h, blocks, M, N, K):
+    """Exact sums (and exact squares of them, below 2^24 after scaling) give the oracle's
+    codes and exponents bit for bit, through each epilogue."""
+    a, b, va, vb = operands(M, N, K, False, True, seed=M)
+    want = va @ vb
+    for epi in ("none", "relu2"):
+        ref = fp8.relu2(want).astype(np.float32).astype(np.float64) if epi == "relu2" else want
+        out = mb.Fp8Matrix(M, N, blocks=blocks, format="e5m2" if epi == "none" else "e4m3")
+        out.codes.fill_(0xEE)
+        mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, out, trans_b=True, epilogue=epi)])
+        c, e = fp8.quantize(ref, out.format, blocks)
+        np.testing.assert_array_equal(exps(out), e)
+        np.testing.assert_array_equal(codes(out), c)
+        assert (out.codes[:, N:] == 0xEE).all()
+    # backward: saved values 0, 1, 4, 16 have exact roots
+    saved = mb.Fp8Matrix(M, N, blocks=blocks)
+    rng = np.random.default_rng(1)
+    vals = fp8.code_values("e4m3")
+    table = np.array([int(np.flatnonzero(vals == v)[0]) for v in (0, 1, 4, 16)], dtype=np.uint8)
+    saved.codes[:, :N] = torch.from_numpy(table[rng.integers(0, 4, (M, N))]).cuda()
+    saved.scales.copy_(torch.from_numpy((127 + 2 * rng.integers(-1, 2, tuple(saved.scales.shape))).astype(np.uint8)))
+    ref = fp8.relu2_backward(want, values(saved))
+    out = mb.Fp8Matrix(M, N, blocks=blocks)
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, out, trans_b=True, epilogue="relu2_backward", saved=saved)])
+    c, e = fp8.quantize(ref, "e4m3", blocks)
+    np.testing.assert_array_equal(exps(out), e)
+    np.testing.assert_array_equal(values(out), fp8.dequantize(c, e, "e4m3", blocks))
+    d = torch.empty(M, N, device="cuda")
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, d, trans_b=True, epilogue="relu2_backward", saved=saved)])
+    np.testing.assert_array_equal(d.double().cpu().numpy(), ref)
+
+
+def test_list_of_products_mixed(h):
+    """Forms, shapes and destinations mixed in one call; more products than one launch takes;
+    empty results and empty contractions among them."""
+    prods, checks = [], []
+    shapes = [(50, 60, 70), (1, 300, 128), (260, 20, 600), (128, 256, 0), (0, 40, 64), (40, 0, 64), (129, 129, 129)]
+    for i in range(21):
+        M, N, K = shapes[i % len(shapes)]
+        ta, tb = bool(i & 1), bool(i & 2)
+        a, b, va, vb = operands(M, N, K, ta, tb, seed=i)
+        d = torch.full((M, N), 3.0, device="cuda")
+        prods.append(mb.Fp8Product(a, b, d, trans_a=ta, trans_b=tb, add=d if i % 3 == 0 else None))
+        checks.append((d, va @ vb + (3.0 if i % 3 == 0 else 0.0)))
+    mb.muon_fp8_matmul(h, prods)
+    assert mb.muon_last_launch_count(h) == 1      # 15 results with entries fit one launch
+    for d, want in checks:
+        np.testing.assert_array_equal(d.double().cpu().numpy(), want)
+    more = []
+    for i in range(35):
+        a, b, va, vb = operands(33 + i, 20, 40 + i, False, True, seed=i)
+        more.append((a, b, torch.empty(33 + i, 20, device="cuda"), va @ vb))
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, d, trans_b=True) for a, b, d, _ in more])
+    for _, _, d, want in more:
+        np.testing.assert_array_equal(d.double().cpu().numpy(), want)
+
+
+def test_column_slices_as_results(h):
+    """q, k and v written into one tensor; odd pitch and offset; the rest stays."""
+    x, w1, vx, vw1 = operands(150, 130, 256, False, True, seed=1)
+    w2 = small_ints(67, 256, "e4m3", "square", 77)
+    big = torch.full((150, 211), 5.0, device="cuda", dtype=torch.float32)
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(x, w1, big[:, 1:131], trans_b=True),
+                           mb.Fp8Product(x, w2, big[:, 131:198], trans_b=True)])
+    got = big.double().cpu().numpy()
+    np.testing.assert_array_equal(got[:, 1:131], vx @ vw1)
+    np.testing.assert_array_equal(got[:, 131:198], vx @ values(w2).T)
+    assert (got[:, 0] == 5).all() and (got[:, 198:] == 5).all()
+
+
+def test_deterministic_and_capturable(h):
+    rng = np.random.default_rng(3)
+    x = torch.from_numpy(rng.standard_normal((4096, 256))).float().cuda()
+    y = torch.from_numpy(rng.standard_normal((4096, 384))).float().cuda()
+    a, b = mb.Fp8Matrix(4096, 256), mb.Fp8Matrix(4096, 384)
+    handle = mb.muon_init(0)
+    d = torch.empty(256, 384, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mb.muon_fp8_quantize(handle, [x, y], [a, b])
+        mb.muon_fp8_matmul(handle, [mb.Fp8Product(a, b, d, trans_a=True)])
+    g.replay()
+    first = d.clone()
+    for _ in range(20):
+        d.zero_()
+        g.replay()
+        assert torch.equal(d, first)
+    eager = torch.empty_like(d)
+    mb.muon_fp8_matmul(handle, [mb.Fp8Product(a, b, eager, trans_a=True)])
+    mb.muon_sync(handle)
+    assert torch.equal(eager, first)
+    # two streams at once, one handle
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [torch.empty_like(d) for _ in s]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st, o in zip(s, outs):
+            mb.muon_fp8_matmul(handle, [mb.Fp8Product(a, b, o, trans_a=True)], stream=st)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, first)
+    del g
+    mb.muon_destroy(handle)
+
+
+def test_refusals(h):
+    a, b = mb.Fp8Matrix(64, 128), mb.Fp8Matrix(96, 128)
+    d = torch.zeros(64, 96, device="cuda")
+
+    def refused(match, **kw):
+        p = dict(a=a, b=b, out=d, trans_b=True)
+        p.update(kw)
+        with pytest.raises(mb.MuonError, match=match) as ei:
+            mb.muon_fp8_matmul(h, [mb.Fp8Product(**p)])
+        assert ei.value.code == mb.MUON_ERR_INVALID_ARG
+
+    refused("op\\(A\\)", trans_b=False)
+    refused("op\\(A\\)", trans_a=True)
+    refused("the product 64 x 96", out=torch.zeros(64, 95, device="cuda"))
+    refused("the product 64 x 96", out=mb.Fp8Matrix(64, 97))
+    refused("c is", add=torch.zeros(63, 96, device="cuda"))
+    refused("saved is", epilogue="relu2_backward", saved=mb.Fp8Matrix(64, 95))
+    refused("square", a=mb.Fp8Matrix(128, 64, blocks="row"), trans_a=True)
+    refused("square", b=mb.Fp8Matrix(128, 96, blocks="row"), trans_b=False)
+    big = torch.zeros(64, 200, device="cuda")
+    refused("overlap", out=big[:, :96], add=big[:, 1:97])
+    sq = mb.Fp8Matrix(128, 128)
+    refused("overlap", a=sq, b=sq, out=sq, trans_b=False)
+    with pytest.raises(mb.MuonError, match="overlap"):
+        mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, d, trans_b=True), mb.Fp8Product(a, b, d, trans_b=True)])
+    # the same operands twice are fine
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, big[:, :96], trans_b=True),
+                           mb.Fp8Product(a, b, big[:, 100:196], trans_b=True)])
+    lib = mb.load_library()
+    assert lib.muon_fp8_matmul(h, None, 1, None) == mb.MUON_ERR_INVALID_ARG
+    raw = (mb.muon_fp8_product * 1)()
+    raw[0].a, raw[0].b, raw[0].trans_b = a.c, b.c, 1
+    assert lib.muon_fp8_matmul(h, raw, 1, None) == mb.MUON_ERR_INVALID_ARG          # no destination
+    raw[0].d = mb.muon_dense(d.data_ptr(), 64, 96, 96, mb.MUON_F32)
+    raw[0].epilogue = 9
+    assert lib.muon_fp8_matmul(h, raw, 1, None) == mb.MUON_ERR_INVALID_ARG
+    assert b"epilogue" in lib.muon_last_error(h)
+    mb.muon_sync(h)
