@@ -215,6 +215,8 @@ def _mode_code(mode) -> int:
 
 def _stream_ptr(stream, device) -> int:
     if stream is None:
+        if isinstance(device, torch.device) and device.index is not None:
+            return torch._C._cuda_getCurrentRawStream(device.index)   # without building a Stream object
         stream = torch.cuda.current_stream(device)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -357,7 +359,7 @@ class Fp8Matrix:
     Allocates ``codes`` (uint8, rows padded to a multiple of 16 bytes) and ``scales`` (uint8)
     unless both are given."""
 
-    __slots__ = ("rows", "cols", "format", "blocks", "codes", "scales", "c")
+    __slots__ = ("rows", "cols", "format", "blocks", "device", "c", "_codes", "_scales", "_buf")
 
     def __init__(self, rows: int, cols: int, format: str = "e4m3", blocks: str = "square", device="cuda",
                  codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None):
@@ -370,11 +372,15 @@ class Fp8Matrix:
             raise ValueError("rows and cols must be >= 0")
         if (codes is None) != (scales is None):
             raise ValueError("give both codes and scales, or neither")
-        bc = (cols + 127) // 128
-        shape = ((rows + 127) // 128, bc) if blocks == "square" else (bc, rows)
+        ld = (cols + 15) // 16 * 16
+        self.rows, self.cols, self.format, self.blocks = rows, cols, format, blocks
         if codes is None:
-            codes = torch.empty(rows, (cols + 15) // 16 * 16, dtype=torch.uint8, device=device)
-            scales = torch.empty(shape, dtype=torch.uint8, device=device)
+            # one allocation: codes, then scales; the tensors over it are made when asked for
+            n_codes, (sr, sc) = rows * ld, self._scale_shape()
+            buf = torch.empty(n_codes + sr * sc, dtype=torch.uint8, device=device)
+            self._buf, self._codes, self._scales, self.device = buf, None, None, buf.device
+            p_codes = buf.data_ptr()
+            p_scales = p_codes + n_codes
         else:
             for t, name in ((codes, "codes"), (scales, "scales")):
                 if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.uint8:
@@ -386,22 +392,34 @@ class Fp8Matrix:
             if rows and cols and ((codes.shape[1] > 1 and codes.stride(1) != 1)
                                   or (rows > 1 and codes.stride(0) < codes.shape[1])):
                 raise ValueError("the codes of a row must be consecutive, and rows must not overlap")
-            if tuple(scales.shape) != shape or not scales.is_contiguous():
-                raise ValueError(f"scales must be a contiguous tensor of shape {shape}")
-        self.rows, self.cols, self.format, self.blocks, self.codes, self.scales = (rows, cols, format, blocks, codes,
-                                                                                  scales)
-        # one row has no pitch of its own: any multiple of 16 that holds it will do
-        ld = codes.stride(0) if rows > 1 else (cols + 15) // 16 * 16
-        self.c = muon_fp8_matrix(codes.data_ptr(), scales.data_ptr(), rows, cols, ld, FP8_FORMATS[format],
-                                 FP8_BLOCKS[blocks])
+            if tuple(scales.shape) != self._scale_shape() or not scales.is_contiguous():
+                raise ValueError(f"scales must be a contiguous tensor of shape {self._scale_shape()}")
+            self._buf, self._codes, self._scales, self.device = None, codes, scales, codes.device
+            p_codes, p_scales = codes.data_ptr(), scales.data_ptr()
+            # one row has no pitch of its own: any multiple of 16 that holds it will do
+            ld = codes.stride(0) if rows > 1 else ld
+        self.c = muon_fp8_matrix(p_codes, p_scales, rows, cols, ld, FP8_FORMATS[format], FP8_BLOCKS[blocks])
+
+    def _scale_shape(self):
+        bc = (self.cols + 127) // 128
+        return ((self.rows + 127) // 128, bc) if self.blocks == "square" else (bc, self.rows)
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            ld = (self.cols + 15) // 16 * 16
+            self._codes = self._buf[:self.rows * ld].view(self.rows, ld)
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            self._scales = self._buf[self.rows * ((self.cols + 15) // 16 * 16):].view(self._scale_shape())
+        return self._scales
 
     @property
     def shape(self):
         return (self.rows, self.cols)
-
-    @property
-    def device(self):
-        return self.codes.device
 
 
 class Fp8Product:
@@ -431,11 +449,19 @@ def _dense(t: torch.Tensor, name: str) -> muon_dense:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor")
-    rows, cols = t.shape
-    if cols > 1 and rows > 0 and t.stride(1) != 1:
+    (rows, cols), (ld, step) = t.shape, t.stride()
+    if step != 1 and cols > 1 and rows > 0:
         raise ValueError(f"{name} must have consecutive columns")
-    ld = t.stride(0) if rows > 1 else cols
+    if rows <= 1:
+        ld = cols
     return muon_dense(t.data_ptr(), rows, cols, ld, _dtype_code(t))
+
+
+def _list(struct, items, convert, name):
+    """HOST array of the items' structs; a pointer to the one struct for a single item."""
+    if len(items) == 1:
+        return ctypes.byref(convert(items[0], name))
+    return (struct * len(items))(*[convert(t, name) for t in items])
 
 
 def _activation(act: str) -> int:
@@ -444,33 +470,32 @@ def _activation(act: str) -> int:
     return ACTIVATIONS[act]
 
 
-def _same_length(**lists) -> int:
-    lens = {len(v) for v in lists.values()}
-    if len(lens) != 1:
-        raise ValueError(f"{', '.join(lists)} must have the same length")
-    return lens.pop()
+def _same_length(names: str, first, *others) -> int:
+    n = len(first)
+    for v in others:
+        if len(v) != n:
+            raise ValueError(f"{names} must have the same length")
+    return n
 
 
 def muon_fp8_quantize(handle, xs: Sequence[torch.Tensor], outs: Sequence[Fp8Matrix], activation: str = "none",
                       stream=None) -> None:
     """outs[i] <- f(xs[i]) in 8 bits (bf16 / fp32 in; f = identity or relu^2): activation
     checkpoints, operands of products, 8-bit copies of weights."""
-    n = _same_length(xs=xs, outs=outs)
+    n = _same_length("xs and outs", xs, outs)
     act = _activation(activation)
     if n == 0:
         return
-    x = (muon_dense * n)(*[_dense(t, "x") for t in xs])
-    o = (muon_fp8_matrix * n)(*[_fp8(m, "out") for m in outs])
+    x, o = _list(muon_dense, xs, _dense, "x"), _list(muon_fp8_matrix, outs, _fp8, "out")
     _check(load_library().muon_fp8_quantize(handle, x, o, n, act, _stream_ptr(stream, xs[0].device)), handle)
 
 
 def muon_fp8_dequantize(handle, xs: Sequence[Fp8Matrix], outs: Sequence[torch.Tensor], stream=None) -> None:
     """outs[i] <- the values of xs[i] (bf16 / fp32 out)."""
-    n = _same_length(xs=xs, outs=outs)
+    n = _same_length("xs and outs", xs, outs)
     if n == 0:
         return
-    x = (muon_fp8_matrix * n)(*[_fp8(m, "x") for m in xs])
-    o = (muon_dense * n)(*[_dense(t, "out") for t in outs])
+    x, o = _list(muon_fp8_matrix, xs, _fp8, "x"), _list(muon_dense, outs, _dense, "out")
     _check(load_library().muon_fp8_dequantize(handle, x, o, n, _stream_ptr(stream, xs[0].device)), handle)
 
 
@@ -478,12 +503,11 @@ def muon_fp8_act_backward(handle, dys: Sequence[torch.Tensor], saved: Sequence[F
                           activation: str = "relu2", stream=None) -> None:
     """dus[i] <- dys[i] * f'(u) from the checkpoint saved[i] = f(u); each of dus is a tensor
     (which may be dys[i] itself) or an Fp8Matrix."""
-    n = _same_length(dys=dys, saved=saved, dus=dus)
+    n = _same_length("dys, saved and dus", dys, saved, dus)
     act = _activation(activation)
     if n == 0:
         return
-    dy = (muon_dense * n)(*[_dense(t, "dy") for t in dys])
-    sv = (muon_fp8_matrix * n)(*[_fp8(m, "saved") for m in saved])
+    dy, sv = _list(muon_dense, dys, _dense, "dy"), _list(muon_fp8_matrix, saved, _fp8, "saved")
     du, du8 = (muon_dense * n)(), (muon_fp8_matrix * n)()
     for i, t in enumerate(dus):
         if isinstance(t, Fp8Matrix):

@@ -34,58 +34,76 @@ __device__ __forceinline__ float f8_scale(uint32_t byte) {
   return byte == 255u ? __uint_as_float(0x7fc00000u) : f8_exp2((int)byte - 127);
 }
 
+constexpr float kF8Inf = __builtin_huge_valf();
+
 // |v| where finite, else 0.
 __device__ __forceinline__ float f8_finite_abs(float v) {
   const float a = fabsf(v);
-  return a < __uint_as_float(0x7f800000u) ? a : 0.f;
+  return a < kF8Inf ? a : 0.f;
 }
 
 // f(u) = max(u, 0)^2; NaN stays NaN.
 __device__ __forceinline__ float f8_relu2(float u) { return u > 0.f ? __fmul_rn(u, u) : (u == u ? 0.f : u); }
-// f'(u) from h = f(u): 2 relu(u) = 2 sqrt(h).
-__device__ __forceinline__ float f8_relu2_slope(float h) { return __fmul_rn(2.f, __fsqrt_rn(h)); }
-
-// 8 scaled values to 8 codes, round to nearest even.  The conversion saturates, so
-// infinities are put right afterwards (NaN in e4m3, infinity in e5m2).
-__device__ __forceinline__ uint2 f8_encode8(const float* v, float inv, bool e5m2) {
-  uint32_t w[2];
-  float s[8];
-  bool inf = false;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    s[i] = __fmul_rn(v[i], inv);
-    inf |= fabsf(v[i]) == __uint_as_float(0x7f800000u);
+// f'(u) = 2 relu(u) = 2 sqrt(h) from h = f(u) = q 2^e: with p the parity of e,
+// 2 sqrt(q 2^p) 2^((e - p) / 2), whose power of two is exact.  The first factor is one of 512
+// numbers (code, parity), kept in shared memory: a lookup and a product per entry in the
+// place of a square root with its rounding (the root took half of the gradient pass: 181 us
+// against 77 us of traffic for 16384 x 6144 bf16).
+constexpr int kF8SlopeTable = 512;
+__device__ __forceinline__ void f8_slope_init(float* table, bool e5m2, int tid, int threads) {
+  for (int i = tid; i < kF8SlopeTable; i += threads) {
+    const uint16_t pair = (uint16_t)(i & 255);
+    uint32_t h2;
+    if (e5m2) asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h2) : "h"(pair));
+    else asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(pair));
+    const float q = __low2float(*reinterpret_cast<const __half2*>(&h2));
+    table[i] = __fmul_rn(2.f, __fsqrt_rn(i >= 256 ? __fmul_rn(2.f, q) : q));
   }
+}
+
+// 8 values times `inv` to 8 codes, round to nearest even.  The conversion saturates, so
+// infinities need f8_encode_inf8 as well.
+template <bool E5M2>
+__device__ __forceinline__ uint2 f8_encode8(const float* v, float inv) {
+  uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     uint16_t lo, hi;
-    if (e5m2) {
-      asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(s[4 * i + 1]), "f"(s[4 * i]));
-      asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(s[4 * i + 3]), "f"(s[4 * i + 2]));
+    const float a = __fmul_rn(v[4 * i], inv), b = __fmul_rn(v[4 * i + 1], inv);
+    const float c = __fmul_rn(v[4 * i + 2], inv), d = __fmul_rn(v[4 * i + 3], inv);
+    if constexpr (E5M2) {
+      asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+      asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
     } else {
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(s[4 * i + 1]), "f"(s[4 * i]));
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(s[4 * i + 3]), "f"(s[4 * i + 2]));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
     }
     w[i] = (uint32_t)lo | ((uint32_t)hi << 16);
-  }
-  if (inf) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (fabsf(v[i]) == __uint_as_float(0x7f800000u)) {
-        const uint32_t c = (v[i] < 0.f ? 0x80u : 0u) | (e5m2 ? 0x7cu : 0x7fu);
-        w[i >> 2] = (w[i >> 2] & ~(0xffu << (8 * (i & 3)))) | (c << (8 * (i & 3)));
-      }
   }
   return make_uint2(w[0], w[1]);
 }
 
+// Puts right the codes of infinite values: NaN in e4m3, infinity in e5m2, sign kept.
+template <bool E5M2>
+__device__ __forceinline__ uint2 f8_encode_inf8(const float* v, uint2 c) {
+  uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (fabsf(v[i]) == kF8Inf) {
+      const uint32_t code = (v[i] < 0.f ? 0x80u : 0u) | (E5M2 ? 0x7cu : 0x7fu);
+      w[i >> 2] = (w[i >> 2] & ~(0xffu << (8 * (i & 3)))) | (code << (8 * (i & 3)));
+    }
+  return make_uint2(w[0], w[1]);
+}
+
 // 8 codes to 8 values times `scale` (both conversions are exact).
-__device__ __forceinline__ void f8_decode8(uint2 c, float scale, bool e5m2, float* v) {
+template <bool E5M2>
+__device__ __forceinline__ void f8_decode8(uint2 c, float scale, float* v) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint16_t pair = (uint16_t)((i < 2 ? c.x : c.y) >> (16 * (i & 1)));
     uint32_t h2;
-    if (e5m2)
+    if constexpr (E5M2)
       asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h2) : "h"(pair));
     else
       asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(pair));
@@ -95,34 +113,113 @@ __device__ __forceinline__ void f8_decode8(uint2 c, float scale, bool e5m2, floa
   }
 }
 
-// 8 consecutive entries (row, col .. col + 7) of a dense matrix; entries at or past `cols`
-// read as 0 and are not written.
-__device__ __forceinline__ void f8_load8(const F8Dense& x, int64_t row, int col, int cols, float* v) {
-  const int64_t at = row * x.ld + col;
+// N groups of 8 consecutive entries of a dense matrix, group i at (row0 + i * step, col):
+// entries outside rows x cols read as 0.  Every load is issued before the first use.
+template <int N, bool BF16>
+__device__ __forceinline__ void f8_load_rows_t(const F8Dense& x, int row0, int step, int rows, int col, int cols,
+                                               float (&v)[N][8]) {
   if (x.vec && col + 8 <= cols) {
-    if (x.bf16) {
-      const uint4 raw = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(x.data) + at);
-      const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&raw);
+    if constexpr (BF16) {
+      uint4 raw[N];
+      const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(x.data) + (int64_t)row0 * x.ld + col;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = __bfloat1622float2(h[i]);
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
+      for (int i = 0; i < N; ++i)
+        raw[i] = row0 + i * step < rows ? *reinterpret_cast<const uint4*>(p + (int64_t)(i * step) * x.ld)
+                                        : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[i][2 * j] = __uint_as_float(w[j] << 16);
+          v[i][2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        }
       }
     } else {
-      const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(x.data) + at);
-      const float4 a = p[0], b = p[1];
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+      const float* p = reinterpret_cast<const float*>(x.data) + (int64_t)row0 * x.ld + col;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+        if (row0 + i * step < rows) {
+          a = reinterpret_cast<const float4*>(p + (int64_t)(i * step) * x.ld)[0];
+          b = reinterpret_cast<const float4*>(p + (int64_t)(i * step) * x.ld)[1];
+        }
+        v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
+        v[i][4] = b.x; v[i][5] = b.y; v[i][6] = b.z; v[i][7] = b.w;
+      }
     }
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[i] = 0.f;
-    if (col + i < cols)
-      v[i] = x.bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(x.data)[at + i])
-                    : reinterpret_cast<const float*>(x.data)[at + i];
+  for (int i = 0; i < N; ++i) {
+    const int64_t at = (int64_t)(row0 + i * step) * x.ld + col;
+    const bool live = row0 + i * step < rows;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[i][j] = 0.f;
+      if (live && col + j < cols)
+        v[i][j] = BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(x.data)[at + j])
+                       : reinterpret_cast<const float*>(x.data)[at + j];
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ void f8_load_rows(const F8Dense& x, int row0, int step, int rows, int col, int cols,
+                                             float (&v)[N][8]) {
+  if (x.bf16) f8_load_rows_t<N, true>(x, row0, step, rows, col, cols, v);
+  else f8_load_rows_t<N, false>(x, row0, step, rows, col, cols, v);
+}
+
+// Rows whose 8-entry groups are not 16-byte aligned: a half warp moves the 128 entries of
+// a row as 8 runs of 16 and trades them for groups of 8 through `xch`, its 128 floats of
+// shared memory, so that memory sees whole sectors (a thread's own 8 entries one by one
+// cost 43 us against 20 us for storing 4999 x 1531 float32).  Both half warps take part.
+constexpr int kF8Xch = 144;  // floats per half warp: 128, and 16 banks between two of them
+template <int N, bool BF16>
+__device__ __forceinline__ void f8_load_rows_xch(const F8Dense& x, int row0, int step, int rows, int col, int cols,
+                                                 float (&v)[N][8], float* xch) {
+  const int l = threadIdx.x & 15, c0 = col - 8 * l + l;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int64_t at = (int64_t)(row0 + i * step) * x.ld + c0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[i][j] = 0.f;
+      if (row0 + i * step < rows && c0 + 16 * j < cols)
+        v[i][j] = BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(x.data)[at + 16 * j])
+                       : reinterpret_cast<const float*>(x.data)[at + 16 * j];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) xch[l + 16 * j] = v[i][j];
+    __syncwarp();
+    const float4 a = *reinterpret_cast<const float4*>(xch + 8 * l), b = *reinterpret_cast<const float4*>(xch + 8 * l + 4);
+    v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
+    v[i][4] = b.x; v[i][5] = b.y; v[i][6] = b.z; v[i][7] = b.w;
+    __syncwarp();
+  }
+}
+template <int N>
+__device__ __forceinline__ void f8_store_rows_xch(const F8Dense& x, int row0, int step, int rows, int col, int cols,
+                                                  const float (&v)[N][8], float* xch) {
+  const int l = threadIdx.x & 15, c0 = col - 8 * l + l;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    *reinterpret_cast<float4*>(xch + 8 * l) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+    *reinterpret_cast<float4*>(xch + 8 * l + 4) = make_float4(v[i][4], v[i][5], v[i][6], v[i][7]);
+    __syncwarp();
+    if (row0 + i * step < rows) {
+      const int64_t at = (int64_t)(row0 + i * step) * x.ld + c0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c0 + 16 * j < cols) {
+          if (x.bf16) reinterpret_cast<__nv_bfloat16*>(x.data)[at + 16 * j] = __float2bfloat16_rn(xch[l + 16 * j]);
+          else reinterpret_cast<float*>(x.data)[at + 16 * j] = xch[l + 16 * j];
+        }
+    }
+    __syncwarp();
   }
 }
 
@@ -152,17 +249,29 @@ __device__ __forceinline__ void f8_store8(const F8Dense& x, int64_t row, int col
     }
 }
 
-// 8 consecutive codes, with the same treatment of the row's end.  Codes are 16-byte
-// aligned with a pitch that is a multiple of 16, so a multiple of 8 columns is 8-byte
-// aligned.
-__device__ __forceinline__ uint2 f8_load_codes8(const F8Mat& m, int64_t row, int col, int cols) {
-  const uint8_t* p = m.codes + row * m.ld + col;
-  if (col + 8 <= cols) return *reinterpret_cast<const uint2*>(p);
-  uint32_t w[2] = {0u, 0u};
+// N groups of 8 consecutive codes, in the manner of f8_load_rows (code 0 outside).  Codes
+// are 16-byte aligned with a pitch that is a multiple of 16, so a multiple of 8 columns is
+// 8-byte aligned.
+template <int N>
+__device__ __forceinline__ void f8_load_code_rows(const F8Mat& m, int row0, int step, int rows, int col, int cols,
+                                                  uint2 (&c)[N]) {
+  const uint8_t* p = m.codes + (int64_t)row0 * m.ld + col;
+  if (col + 8 <= cols) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (col + i < cols) w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
-  return make_uint2(w[0], w[1]);
+    for (int i = 0; i < N; ++i)
+      c[i] = row0 + i * step < rows ? *reinterpret_cast<const uint2*>(p + (int64_t)(i * step) * m.ld)
+                                    : make_uint2(0u, 0u);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint32_t w[2] = {0u, 0u};
+    const bool live = row0 + i * step < rows;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (live && col + j < cols) w[j >> 2] |= (uint32_t)p[(int64_t)(i * step) * m.ld + j] << (8 * (j & 3));
+    c[i] = make_uint2(w[0], w[1]);
+  }
 }
 
 __device__ __forceinline__ void f8_store_codes8(const F8Mat& m, int64_t row, int col, int cols, uint2 c) {
@@ -179,6 +288,100 @@ __device__ __forceinline__ void f8_store_codes8(const F8Mat& m, int64_t row, int
 // Where the scale byte of entry (row, 128-column block kb) lives.
 __device__ __forceinline__ uint8_t* f8_scale_at(const F8Mat& m, int row, int kb) {
   return m.row_blocks ? m.scales + (int64_t)kb * m.s_col + row : m.scales + (int64_t)(row / kFp8Block) * m.s_row + kb;
+}
+
+// v[i] *= f'(u) from the checkpoint's entries at (row0 + i * step, col); table: f8_slope_init.
+template <int N>
+__device__ __forceinline__ void f8_times_slope(const F8Mat& saved, const float* table, int row0, int step, int rows,
+                                               int col, int cols, float (&v)[N][8]) {
+  uint2 c[N];
+  uint32_t sb[N];
+  f8_load_code_rows<N>(saved, row0, step, rows, col, cols, c);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    sb[i] = row0 + i * step < rows && col < cols ? *f8_scale_at(saved, row0 + i * step, col / kFp8Block) : 127u;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int e = (int)sb[i] - 127, parity = e & 1;
+    const float scale = sb[i] == 255u ? __uint_as_float(0x7fc00000u) : f8_exp2((e - parity) / 2);
+    const float* t = table + 256 * parity;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[i][j] = __fmul_rn(__fmul_rn(t[((j < 4 ? c[i].x : c[i].y) >> (8 * (j & 3))) & 255u], scale), v[i][j]);
+  }
+}
+
+// Largest magnitude of v[i] (NaN is passed over, infinity is not).
+template <int N>
+__device__ __forceinline__ void f8_row_max(const float (&v)[N][8], float (&rmax)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    rmax[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) rmax[i] = fmaxf(rmax[i], fabsf(v[i][j]));
+  }
+}
+// The same over finite entries.
+template <int N>
+__device__ __forceinline__ void f8_row_max_finite(const float (&v)[N][8], float (&rmax)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    rmax[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) rmax[i] = fmaxf(rmax[i], f8_finite_abs(v[i][j]));
+  }
+}
+__device__ __forceinline__ float f8_half_warp_max(float m) {
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  return m;
+}
+
+// Stores the codes of v[i] at (row0 + i * step, col); inv[i]: 2^-e of the row's block;
+// inf: some entry may be infinite.
+template <int N, bool E5M2>
+__device__ __forceinline__ void f8_store_rows_t(const F8Mat& m, int row0, int step, int rows, int col, int cols,
+                                                const float (&v)[N][8], const float (&inv)[N], bool inf) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint2 c = f8_encode8<E5M2>(v[i], inv[i]);
+    if (inf) c = f8_encode_inf8<E5M2>(v[i], c);
+    if (row0 + i * step < rows && col < cols) f8_store_codes8(m, row0 + i * step, col, cols, c);
+  }
+}
+template <int N>
+__device__ __forceinline__ void f8_store_rows(const F8Mat& m, int row0, int step, int rows, int col, int cols,
+                                              const float (&v)[N][8], const float (&inv)[N], bool inf) {
+  if (m.e5m2) f8_store_rows_t<N, true>(m, row0, step, rows, col, cols, v, inv, inf);
+  else f8_store_rows_t<N, false>(m, row0, step, rows, col, cols, v, inv, inf);
+}
+
+// Row blocks: each half warp holds whole rows of 128 columns.
+template <int N>
+__device__ __forceinline__ void f8_quantize_rows(const F8Mat& m, int row0, int step, int rows, int col, int cols,
+                                                 const float (&v)[N][8]) {
+  float rmax[N], inv[N];
+  f8_row_max<N>(v, rmax);
+  bool inf = false;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    rmax[i] = f8_half_warp_max(rmax[i]);
+    inf |= rmax[i] == kF8Inf;
+  }
+  inf = __any_sync(0xffffffffu, inf);
+  if (inf) {
+    f8_row_max_finite<N>(v, rmax);
+#pragma unroll
+    for (int i = 0; i < N; ++i) rmax[i] = f8_half_warp_max(rmax[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int e = f8_exponent(rmax[i], m.e5m2);
+    inv[i] = f8_exp2(-e);
+    if ((threadIdx.x & 15) == 0 && row0 + i * step < rows)
+      *f8_scale_at(m, row0 + i * step, col / kFp8Block) = (uint8_t)(e + 127);
+  }
+  f8_store_rows<N>(m, row0, step, rows, col, cols, v, inv, inf);
 }
 
 }  // namespace

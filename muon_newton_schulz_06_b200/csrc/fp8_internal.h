@@ -44,16 +44,22 @@ struct F8Pass {
   int32_t blocks_c;     // 128-column blocks per row of blocks
   int32_t block_begin;  // first block of this matrix inside the launch
 };
+// A launch's parameters travel with it, so calls of a few matrices use a smaller struct (a
+// launch copies all of it: 17 KB for 96 matrices).
 constexpr int kMaxF8Passes = 96;
-struct F8PassParams {
-  F8Pass m[kMaxF8Passes];
+constexpr int kF8FewPasses = 4;
+template <int N>
+struct F8PassParamsN {
+  F8Pass m[N];
   int n;
   int total_blocks;
   int relu2;
 };
-static_assert(sizeof(F8PassParams) <= 32764, "parameters of the block passes must fit the kernel parameter space");
+static_assert(sizeof(F8PassParamsN<kMaxF8Passes>) <= 32764,
+              "parameters of the block passes must fit the kernel parameter space");
 
-cudaError_t launch_fp8_pass(int op, const F8PassParams& p, cudaStream_t st);
+cudaError_t launch_fp8_pass(int op, const F8PassParamsN<kF8FewPasses>& p, cudaStream_t st);
+cudaError_t launch_fp8_pass(int op, const F8PassParamsN<kMaxF8Passes>& p, cudaStream_t st);
 
 // ------------------------------------------------------------------ products
 
@@ -79,18 +85,22 @@ struct F8Product {
   int32_t tile_begin;      // first tile inside the launch
 };
 constexpr int kMaxF8Products = 16;
-struct __align__(64) F8GemmParams {
-  CUtensorMap map_a[kMaxF8Products];
-  CUtensorMap map_b[kMaxF8Products];
-  F8Product p[kMaxF8Products];
+constexpr int kF8FewProducts = 3;
+template <int N>
+struct __align__(64) F8GemmParamsN {
+  CUtensorMap map_a[N];
+  CUtensorMap map_b[N];
+  F8Product p[N];
   int n;
   int total_tiles;
   int* status;
 };
-static_assert(sizeof(F8GemmParams) <= 32764, "parameters of the 8-bit products must fit the kernel parameter space");
+static_assert(sizeof(F8GemmParamsN<kMaxF8Products>) <= 32764,
+              "parameters of the 8-bit products must fit the kernel parameter space");
 
 // 128 x 128 tiles, one CTA each; `split` CTAs (a cluster: 1, 2, 4 or 8) share a tile's
 // contraction and join their sums through distributed shared memory.
-cudaError_t launch_fp8_gemm_tile(const F8GemmParams& p, int split, cudaStream_t st);
+cudaError_t launch_fp8_gemm_tile(const F8GemmParamsN<kF8FewProducts>& p, int split, cudaStream_t st);
+cudaError_t launch_fp8_gemm_tile(const F8GemmParamsN<kMaxF8Products>& p, int split, cudaStream_t st);
 
 }  // namespace muon

@@ -21,6 +21,8 @@
 //
 // Every mbarrier wait is bounded; on expiry the kernel writes kDevTimeout to the status
 // word, lets its copies and MMAs drain, frees tensor memory and returns.
+#include <atomic>
+
 #include "fp8_blocks.cuh"
 #include "fp8_tc.cuh"
 
@@ -37,7 +39,7 @@ constexpr uint32_t kTSfSetBytes = 2 * kF8SfBytes;      // A words, B words
 constexpr int kTPitch = kT + 4;                        // floats per staged row
 constexpr uint32_t kTRing = kTStages * kTStageBytes;
 static_assert(kT * kTPitch * 4 <= kTRing, "the staged tile reuses the ring");
-constexpr uint32_t kTSmem = kTRing + kTSfSets * kTSfSetBytes + 256 + 1024;
+constexpr uint32_t kTSmem = kTRing + kTSfSets * kTSfSetBytes + 256 + kF8SlopeTable * 4 + 1024;
 constexpr uint32_t kTTmemCols = 256;  // 128 accumulator columns, 2 x 8 columns of scales
 constexpr uint32_t kTSfCol = 128;
 
@@ -60,28 +62,31 @@ __device__ __forceinline__ float ld_cluster_f1(uint32_t addr) {
   return v;
 }
 
-// What follows the sum for 8 consecutive entries (row, col ..): addend, activation or its
-// gradient.
-__device__ __forceinline__ void f8_finish8(const F8Product& g, int row, int col, float* v) {
+// What follows the sum, for N groups of 8 consecutive entries at (row0 + i * step, col):
+// addend, activation or its gradient.
+template <int N>
+__device__ __forceinline__ void f8_finish(const F8Product& g, const float* slope, int row0, int step, int row_end, int col,
+                                          float (&v)[N][8]) {
   if (g.c.data != nullptr) {
-    float c[8];
-    f8_load8(g.c, row, col, g.n, c);
+    float c[N][8];
+    f8_load_rows<N>(g.c, row0, step, row_end, col, g.n, c);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += c[j];
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] += c[i][j];
   }
   if (g.epi == kF8EpiRelu2) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = f8_relu2(v[j]);
-  } else if (g.epi == kF8EpiRelu2Backward) {
-    float h[8];
-    f8_decode8(f8_load_codes8(g.saved, row, col, g.n), f8_scale(*f8_scale_at(g.saved, row, col / kFp8Block)),
-               g.saved.e5m2, h);
+    for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(f8_relu2_slope(h[j]), v[j]);
+      for (int j = 0; j < 8; ++j) v[i][j] = f8_relu2(v[i][j]);
+  } else if (g.epi == kF8EpiRelu2Backward) {
+    f8_times_slope<N>(g.saved, slope, row0, step, row_end, col, g.n, v);
   }
 }
 
-__global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_constant__ F8GemmParams p) {
+template <typename Params>
+__global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sf_smem = smem + kTRing;
@@ -94,6 +99,7 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* cta_max = reinterpret_cast<float*>(tmem_slot + 2);  // this CTA's block maximum
   float* warp_max = cta_max + 1;                             // [8]
+  float* slope = reinterpret_cast<float*>(sf_smem + kTSfSets * kTSfSetBytes + 256);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -110,6 +116,7 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
   const int per = (nkb_all + split - 1) / split;
   const int kb_begin = min(nkb_all, rank * per), nkb = min(nkb_all, kb_begin + per) - kb_begin;
 
+  if (g.epi == kF8EpiRelu2Backward) f8_slope_init(slope, g.saved.e5m2, threadIdx.x, kTThreads);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kTStages; ++s) {
       mbar_init(&full[s], 1);
@@ -271,81 +278,125 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
     }
   };
 
+  // rows of this CTA end at row_end; entries past the matrix are kept at 0
+  const int row0 = row_t + rank * rows_here + (threadIdx.x >> 4);
+  const int row_end = min(g.m, row_t + (rank + 1) * rows_here);
   if (g.d8.codes == nullptr) {
     for (int i = 0; i < iters; ++i) {
-      const int rl = rank * rows_here + 16 * i + (threadIdx.x >> 4);
-      const int row = row_t + rl;
-      if (row >= g.m || col >= g.n) continue;
-      float v[8];
-      fetch(rl, v);
-      f8_finish8(g, row, col, v);
-      f8_store8(g.d, row, col, g.n, v);
+      const int row = row0 + 16 * i;
+      float v[1][8];
+      fetch(row - row_t, v[0]);
+      f8_finish<1>(g, slope, row, 16, row_end, col, v);
+      if (g.d.vec) {
+        if (row < row_end && col < g.n) f8_store8(g.d, row, col, g.n, v[0]);
+      } else {  // through this CTA's own row of the staged tile, which no peer reads
+        f8_store_rows_xch<1>(g.d, row, 16, row_end, col, g.n, v, stage + (row - row_t) * kTPitch);
+      }
     }
   } else {
-    const bool e5m2 = g.d8.e5m2;
-    float v[8][8];
-    float rmax[8];
+    // finished values go back to this CTA's own rows of the staged tile (no peer reads
+    // those), 4 rows per thread at a time, until the block's maximum is known
+    auto put = [&](int rl, const float* v) {
+      *reinterpret_cast<float4*>(stage + rl * kTPitch + cl) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(stage + rl * kTPitch + cl + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    };
+    auto get = [&](int rl, float* v) {
+      const float4 x = *reinterpret_cast<const float4*>(stage + rl * kTPitch + cl);
+      const float4 y = *reinterpret_cast<const float4*>(stage + rl * kTPitch + cl + 4);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+      v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+    };
+    constexpr int kC = 4;
+    float vmax = 0.f;
+    for (int i0 = 0; i0 < iters; i0 += kC) {
+      float v[kC][8], rmax[kC];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      rmax[i] = 0.f;
-      if (i < iters) {
-        const int rl = rank * rows_here + 16 * i + (threadIdx.x >> 4);
-        const int row = row_t + rl;
-        if (row < g.m && col < g.n) {
-          fetch(rl, v[i]);
-          f8_finish8(g, row, col, v[i]);
+      for (int i = 0; i < kC; ++i) {
+        const int row = row0 + 16 * (i0 + i);
+        if (row < row_end && col < g.n) {
+          fetch(row - row_t, v[i]);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (col + j < g.n) rmax[i] = fmaxf(rmax[i], f8_finite_abs(v[i][j]));
+            if (col + j >= g.n) v[i][j] = 0.f;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+        }
+      }
+      f8_finish<kC>(g, slope, row0 + 16 * i0, 16, row_end, col, v);
+      if (g.d8.row_blocks) {
+        f8_quantize_rows<kC>(g.d8, row0 + 16 * i0, 16, row_end, col, g.n, v);
+      } else {
+        f8_row_max<kC>(v, rmax);
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+          vmax = fmaxf(vmax, rmax[i]);
+          if (row0 + 16 * (i0 + i) < row_end) put(row0 + 16 * (i0 + i) - row_t, v[i]);
         }
       }
     }
-    float inv = 1.f;
     if (!g.d8.row_blocks) {
-      float amax = 0.f;
+      // maximum over the tile, then over the cluster
+      auto tile_max = [&](float m) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, rmax[i]);
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        __syncthreads();
+        if (lane == 0) warp_max[warp] = m;
+        __syncthreads();
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-      if (lane == 0) warp_max[warp] = amax;
-      __syncthreads();
+        for (int w = 0; w < kTThreads / 32; ++w) m = fmaxf(m, warp_max[w]);
+        if (split > 1) {
+          if (threadIdx.x == 0) *cta_max = m;
+          __syncwarp();
+          cluster_sync_all();
+          for (int r = 0; r < split; ++r) m = fmaxf(m, ld_cluster_f1(peer_addr(smem_u32(cta_max), (uint32_t)r)));
+          __syncwarp();
+          cluster_sync_all();  // read everywhere before it is written again
+        }
+        return m;
+      };
+      float amax = tile_max(vmax);
+      const bool inf = amax == kF8Inf;
+      if (inf) {  // once more over finite entries
+        vmax = 0.f;
+        for (int i = 0; i < iters; ++i)
+          if (row0 + 16 * i < row_end) {
+            float v[8];
+            get(row0 + 16 * i - row_t, v);
 #pragma unroll
-      for (int w = 0; w < kTThreads / 32; ++w) amax = fmaxf(amax, warp_max[w]);
-      if (split > 1) {
-        if (threadIdx.x == 0) *cta_max = amax;
-        __syncwarp();
-        cluster_sync_all();
-        for (int r = 0; r < split; ++r) amax = fmaxf(amax, ld_cluster_f1(peer_addr(smem_u32(cta_max), (uint32_t)r)));
+            for (int j = 0; j < 8; ++j) vmax = fmaxf(vmax, f8_finite_abs(v[j]));
+          }
+        amax = tile_max(vmax);
       }
-      const int e = f8_exponent(amax, e5m2);
+      const int e = f8_exponent(amax, g.d8.e5m2);
       if (threadIdx.x == 0 && rank == 0) *f8_scale_at(g.d8, row_t, tn) = (uint8_t)(e + 127);
-      inv = f8_exp2(-e);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i >= iters) break;
-      const int row = row_t + rank * rows_here + 16 * i + (threadIdx.x >> 4);
-      if (g.d8.row_blocks) {
-        float amax = rmax[i];
-#pragma unroll
-        for (int d = 8; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-        const int e = f8_exponent(amax, e5m2);
-        if (row < g.m && (threadIdx.x & 15) == 0) *f8_scale_at(g.d8, row, tn) = (uint8_t)(e + 127);
-        inv = f8_exp2(-e);
-      }
-      if (row < g.m && col < g.n) f8_store_codes8(g.d8, row, col, g.n, f8_encode8(v[i], inv, e5m2));
+      const float inv[1] = {f8_exp2(-e)};
+      for (int i = 0; i < iters; ++i)
+        if (row0 + 16 * i < row_end) {
+          float v[1][8];
+          get(row0 + 16 * i - row_t, v[0]);
+          f8_store_rows<1>(g.d8, row0 + 16 * i, 16, row_end, col, g.n, v, inv, inf);
+        }
     }
   }
   __syncwarp();
   if (split > 1) cluster_sync_all();  // peers have read this CTA's partial tile and maximum
 }
 
-}  // namespace
-
-cudaError_t launch_fp8_gemm_tile(const F8GemmParams& p, int split, cudaStream_t st) {
+template <typename Params>
+cudaError_t launch_tile(const Params& p, int split, cudaStream_t st) {
   if (p.total_tiles == 0) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(fp8_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTSmem);
+  // once per device: the kernel's shared memory is above the default limit
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (!(ready.load(std::memory_order_relaxed) & bit) || bit == 0) {
+    e = cudaFuncSetAttribute(fp8_tile_kernel<Params>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTSmem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.total_tiles * split));
   cfg.blockDim = dim3(kTThreads);
@@ -358,7 +409,16 @@ cudaError_t launch_fp8_gemm_tile(const F8GemmParams& p, int split, cudaStream_t 
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fp8_tile_kernel, p);
+  return cudaLaunchKernelEx(&cfg, fp8_tile_kernel<Params>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_gemm_tile(const F8GemmParamsN<kF8FewProducts>& p, int split, cudaStream_t st) {
+  return launch_tile(p, split, st);
+}
+cudaError_t launch_fp8_gemm_tile(const F8GemmParamsN<kMaxF8Products>& p, int split, cudaStream_t st) {
+  return launch_tile(p, split, st);
 }
 
 }  // namespace muon

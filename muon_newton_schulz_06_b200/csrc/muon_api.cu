@@ -1227,9 +1227,12 @@ muon_status muon_init(muon_handle_t* out, int device) {
     return MUON_ERR_CUDA;
   }
   if (device < 0 || device >= count) return MUON_ERR_INVALID_ARG;
-  cudaDeviceProp prop;
-  if (cudaGetDeviceProperties(&prop, device) != cudaSuccess) return MUON_ERR_CUDA;
-  if (prop.major != 10 || prop.minor != 0) return MUON_ERR_UNSUPPORTED;
+  int major = 0, minor = 0, sm_count = 0;  // single attributes: the whole property struct takes about 1 ms
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sm_count, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
+    return MUON_ERR_CUDA;
+  if (major != 10 || minor != 0) return MUON_ERR_UNSUPPORTED;
   void* fn = nullptr;
   cudaDriverEntryPointQueryResult q;
   if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) != cudaSuccess ||
@@ -1238,7 +1241,7 @@ muon_status muon_init(muon_handle_t* out, int device) {
   muon_handle* h = new (std::nothrow) muon_handle();
   if (!h) return MUON_ERR_OOM;
   h->device = device;
-  h->sm_count = prop.multiProcessorCount;
+  h->sm_count = sm_count;
   h->encode = reinterpret_cast<EncodeTiledFn>(fn);
   const char* lg = getenv("MUON_LOG");
   h->log = lg != nullptr && lg[0] != '\0' && strcmp(lg, "0") != 0;
@@ -1246,7 +1249,11 @@ muon_status muon_init(muon_handle_t* out, int device) {
   h->debug = dbg != nullptr && dbg[0] != '\0' && strcmp(dbg, "0") != 0;
   const char* nv = getenv("MUON_NVTX");
   h->nvtx = nv != nullptr && nv[0] != '\0' && strcmp(nv, "0") != 0;
-  if (h->log) fprintf(stderr, "muon: handle on device %d (%s, %d SMs)\n", device, prop.name, h->sm_count);
+  if (h->log) {
+    cudaDeviceProp prop;
+    if (cudaGetDeviceProperties(&prop, device) != cudaSuccess) prop.name[0] = '\0';
+    fprintf(stderr, "muon: handle on device %d (%s, %d SMs)\n", device, prop.name, h->sm_count);
+  }
   *out = h;
   return MUON_OK;
 }

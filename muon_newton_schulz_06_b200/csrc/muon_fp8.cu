@@ -1,7 +1,6 @@
 // Host side of the 8-bit operators: argument checks, kernel parameters and tensor maps,
 // launches.  Nothing is kept between calls but the handle's status word.
 #include <algorithm>
-#include <new>
 #include <vector>
 
 #include <nvtx3/nvToolsExt.h>
@@ -174,7 +173,34 @@ struct NvtxScope {
   }
 };
 
-// Checks and then runs one list of block passes, at most kMaxF8Passes matrices a launch.
+template <int N>
+muon_status launch_passes(muon_handle* h, int op, int kind, const std::vector<F8Pass>& passes, int relu2,
+                          cudaStream_t st) {
+  F8PassParamsN<N> p;
+  p.relu2 = relu2;
+  for (size_t b = 0; b < passes.size();) {
+    int64_t total = 0;
+    p.n = 0;
+    for (; b < passes.size() && p.n < N; ++b) {
+      const int64_t nb = blocks_of(passes[b].rows) * (int64_t)passes[b].blocks_c;
+      if (p.n > 0 && total + nb > INT32_MAX) break;
+      F8Pass& m = p.m[p.n++];
+      m = passes[b];
+      m.block_begin = (int32_t)total;
+      total += nb;
+    }
+    if (total > INT32_MAX) return fail(h, MUON_ERR_UNSUPPORTED, "a matrix has more than 2^31 - 1 blocks");
+    p.total_blocks = (int)total;
+    prof_begin(h, st, kFp8KindBase + kind);
+    const cudaError_t e = launch_fp8_pass(op, p, st);
+    prof_end(h, kFp8KindBase + kind, st);
+    if (e != cudaSuccess) return cuda_fail(h, e, "8-bit pass launch");
+    h->last_launches++;
+  }
+  return MUON_OK;
+}
+
+// Checks and then runs one list of block passes.
 muon_status run_passes(Call& call, int op, int kind, const std::vector<F8Pass>& passes, muon_activation act,
                        cudaStream_t st) {
   muon_handle* h = call.h;
@@ -183,35 +209,10 @@ muon_status run_passes(Call& call, int op, int kind, const std::vector<F8Pass>& 
   if ((s = ensure_fp8(h))) return s;
   if ((s = poll_status(h, false))) return s;
   h->last_launches = 0;
-  F8PassParams* p = new (std::nothrow) F8PassParams();
-  if (!p) return fail(h, MUON_ERR_OOM, "host allocation of the launch parameters failed");
-  p->relu2 = act == MUON_ACT_RELU2;
-  for (size_t b = 0; b < passes.size();) {
-    int64_t total = 0;
-    p->n = 0;
-    for (; b < passes.size() && p->n < kMaxF8Passes; ++b) {
-      const int64_t nb = blocks_of(passes[b].rows) * (int64_t)passes[b].blocks_c;
-      if (p->n > 0 && total + nb > INT32_MAX) break;
-      F8Pass& m = p->m[p->n++];
-      m = passes[b];
-      m.block_begin = (int32_t)total;
-      total += nb;
-    }
-    if (total > INT32_MAX) {
-      delete p;
-      return fail(h, MUON_ERR_UNSUPPORTED, "a matrix has more than 2^31 - 1 blocks");
-    }
-    p->total_blocks = (int)total;
-    prof_begin(h, st, kFp8KindBase + kind);
-    const cudaError_t e = launch_fp8_pass(op, *p, st);
-    prof_end(h, kFp8KindBase + kind, st);
-    if (e != cudaSuccess) {
-      delete p;
-      return cuda_fail(h, e, "8-bit pass launch");
-    }
-    h->last_launches++;
-  }
-  delete p;
+  const int relu2 = act == MUON_ACT_RELU2;
+  s = passes.size() <= kF8FewPasses ? launch_passes<kF8FewPasses>(h, op, kind, passes, relu2, st)
+                                    : launch_passes<kMaxF8Passes>(h, op, kind, passes, relu2, st);
+  if (s) return s;
   return finish_fp8(h, st);
 }
 
@@ -275,6 +276,56 @@ int choose_split(int64_t tiles, int64_t kb, int sm_count) {
   int split = 1;
   while (split < 8 && tiles * split * 2 <= 2 * sm_count && kb >= 4 * split) split *= 2;
   return split;
+}
+
+// The products products[live[..]], at most N per launch.
+template <int N>
+muon_status launch_products(muon_handle* h, const muon_fp8_product* products, const std::vector<int>& live,
+                            cudaStream_t st) {
+  F8GemmParamsN<N> p;
+  p.status = h->fp8_status_dev;
+  for (size_t b = 0; b < live.size();) {
+    int64_t tiles = 0, min_kb = INT64_MAX;
+    p.n = 0;
+    for (; b < live.size() && p.n < N; ++b) {
+      const muon_fp8_product& q = products[live[b]];
+      F8Product g = {};
+      g.m = (int32_t)(q.trans_a ? q.a.cols : q.a.rows);
+      g.k = (int32_t)(q.trans_a ? q.a.rows : q.a.cols);
+      g.n = (int32_t)(q.trans_b ? q.b.rows : q.b.cols);
+      g.tiles_m = (int32_t)blocks_of(g.m);
+      g.tiles_n = (int32_t)blocks_of(g.n);
+      const int64_t t = (int64_t)g.tiles_m * g.tiles_n;
+      if (t > INT32_MAX / 8) return fail(h, MUON_ERR_UNSUPPORTED, "item %d: the result has too many tiles", live[b]);
+      if (p.n > 0 && tiles + t > INT32_MAX / 8) break;
+      g.a_mn = q.trans_a ? 1 : 0;
+      g.b_mn = q.trans_b ? 0 : 1;
+      g.a_e5m2 = q.a.format == MUON_E5M2;
+      g.b_e5m2 = q.b.format == MUON_E5M2;
+      g.sa = scales_of(q.a, g.a_mn);
+      g.sb = scales_of(q.b, g.b_mn);
+      if (q.d.data) g.d = kernel_dense(q.d);
+      else g.d8 = kernel_fp8(q.d8);
+      if (q.c.data) g.c = kernel_dense(q.c);
+      g.epi = (int32_t)q.epilogue;
+      if (q.epilogue == MUON_EPI_RELU2_BACKWARD) g.saved = kernel_fp8(q.saved);
+      g.tile_begin = (int32_t)tiles;
+      muon_status s;
+      if (g.k > 0 && ((s = encode_codes(h, &p.map_a[p.n], q.a)) || (s = encode_codes(h, &p.map_b[p.n], q.b))))
+        return s;
+      p.p[p.n++] = g;
+      tiles += t;
+      min_kb = std::min(min_kb, blocks_of(g.k));
+    }
+    p.total_tiles = (int)tiles;
+    const int split = choose_split(tiles, min_kb, h->sm_count);
+    prof_begin(h, st, kFp8KindBase + MUON_FP8_KIND_MATMUL);
+    const cudaError_t e = launch_fp8_gemm_tile(p, split, st);
+    prof_end(h, kFp8KindBase + MUON_FP8_KIND_MATMUL, st);
+    if (e != cudaSuccess) return cuda_fail(h, e, "8-bit product launch");
+    h->last_launches++;
+  }
+  return MUON_OK;
 }
 
 }  // namespace
@@ -433,58 +484,9 @@ muon_status muon_fp8_matmul(muon_handle_t h, const muon_fp8_product* products, i
   if ((s = ensure_fp8(h))) return s;
   if ((s = poll_status(h, false))) return s;
   h->last_launches = 0;
-  F8GemmParams* p = new (std::nothrow) F8GemmParams();
-  if (!p) return fail(h, MUON_ERR_OOM, "host allocation of the launch parameters failed");
-  for (size_t b = 0; b < live.size();) {
-    int64_t tiles = 0, min_kb = INT64_MAX;
-    p->n = 0;
-    for (; b < live.size() && p->n < kMaxF8Products; ++b) {
-      const muon_fp8_product& q = products[live[b]];
-      F8Product g = {};
-      g.m = (int32_t)(q.trans_a ? q.a.cols : q.a.rows);
-      g.k = (int32_t)(q.trans_a ? q.a.rows : q.a.cols);
-      g.n = (int32_t)(q.trans_b ? q.b.rows : q.b.cols);
-      g.tiles_m = (int32_t)blocks_of(g.m);
-      g.tiles_n = (int32_t)blocks_of(g.n);
-      const int64_t t = (int64_t)g.tiles_m * g.tiles_n;
-      if (t > INT32_MAX / 8) {
-        delete p;
-        return fail(h, MUON_ERR_UNSUPPORTED, "item %d: the result has too many tiles", live[b]);
-      }
-      if (p->n > 0 && tiles + t > INT32_MAX / 8) break;
-      g.a_mn = q.trans_a ? 1 : 0;
-      g.b_mn = q.trans_b ? 0 : 1;
-      g.a_e5m2 = q.a.format == MUON_E5M2;
-      g.b_e5m2 = q.b.format == MUON_E5M2;
-      g.sa = scales_of(q.a, g.a_mn);
-      g.sb = scales_of(q.b, g.b_mn);
-      if (q.d.data) g.d = kernel_dense(q.d);
-      else g.d8 = kernel_fp8(q.d8);
-      if (q.c.data) g.c = kernel_dense(q.c);
-      g.epi = (int32_t)q.epilogue;
-      if (q.epilogue == MUON_EPI_RELU2_BACKWARD) g.saved = kernel_fp8(q.saved);
-      g.tile_begin = (int32_t)tiles;
-      if (g.k > 0 && ((s = encode_codes(h, &p->map_a[p->n], q.a)) || (s = encode_codes(h, &p->map_b[p->n], q.b)))) {
-        delete p;
-        return s;
-      }
-      p->p[p->n++] = g;
-      tiles += t;
-      min_kb = std::min(min_kb, blocks_of(g.k));
-    }
-    p->total_tiles = (int)tiles;
-    p->status = h->fp8_status_dev;
-    const int split = choose_split(tiles, min_kb, h->sm_count);
-    prof_begin(h, st, kFp8KindBase + MUON_FP8_KIND_MATMUL);
-    const cudaError_t e = launch_fp8_gemm_tile(*p, split, st);
-    prof_end(h, kFp8KindBase + MUON_FP8_KIND_MATMUL, st);
-    if (e != cudaSuccess) {
-      delete p;
-      return cuda_fail(h, e, "8-bit product launch");
-    }
-    h->last_launches++;
-  }
-  delete p;
+  s = live.size() <= kF8FewProducts ? launch_products<kF8FewProducts>(h, products, live, st)
+                                    : launch_products<kMaxF8Products>(h, products, live, st);
+  if (s) return s;
   return finish_fp8(h, st);
 }
 
