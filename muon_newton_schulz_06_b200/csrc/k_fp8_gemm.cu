@@ -11,7 +11,7 @@
 // Tile kernel: one CTA per 128 x 128 tile of D, 256 threads:
 //   warp 0   TMA producer: 3-stage ring of 128 x 128 code tiles of A and B (16 KB each)
 //   warp 1   tensor memory, MMA issue (one thread)
-//   warp 2   scale words of both operands, one set per 512 codes, two sets in flight
+//   warps 2, 3  scale words of both operands, one set per 512 codes, four sets in flight
 //   all      epilogue: the fp32 tile goes through shared memory (the ring's space), then
 //            half a warp per row finishes 8 columns per thread, as the block passes do
 // With few tiles, a cluster of 2, 4 or 8 CTAs splits a tile's contraction: every CTA
@@ -34,7 +34,7 @@ constexpr int kTThreads = 256;
 constexpr int kTStages = 3;
 constexpr uint32_t kTOperand = kT * kF8K;              // 16 KB
 constexpr uint32_t kTStageBytes = 2 * kTOperand;
-constexpr int kTSfSets = 2;
+constexpr int kTSfSets = 4;                            // in shared memory; two in tensor memory
 constexpr uint32_t kTSfSetBytes = 2 * kF8SfBytes;      // A words, B words
 constexpr int kTPitch = kT + 4;                        // floats per staged row
 constexpr uint32_t kTRing = kTStages * kTStageBytes;
@@ -148,22 +148,24 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
   };
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       const CUtensorMap* ma = &p.map_a[gi];
       const CUtensorMap* mb = &p.map_b[gi];
+      const uint32_t ring = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
+      const int k0 = kb_begin * kF8K;
+      int ax = g.a_mn ? row_t : k0, ay = g.a_mn ? k0 : row_t, bx = g.b_mn ? col_t : k0, by = g.b_mn ? k0 : col_t;
+      const int adx = g.a_mn ? 0 : kF8K, ady = g.a_mn ? kF8K : 0, bdx = g.b_mn ? 0 : kF8K, bdy = g.b_mn ? kF8K : 0;
+      uint32_t stage = 0, phase = 0;
       int issued = 0;
       bool ok = true;
-      for (int i = 0; i < nkb; ++i) {
-        const int s = i % kTStages;
-        if (!mbar_wait(&empty[s], (uint32_t)((i / kTStages) & 1) ^ 1u, abort_flag)) { ok = false; break; }
-        mbar_arrive_expect_tx(&full[s], kTStageBytes);
-        const uint32_t a_dst = smem_u32(smem + s * kTStageBytes);
-        const int k0 = (kb_begin + i) * kF8K;
-        if (g.a_mn) tma_load_2d_local(a_dst, ma, &full[s], row_t, k0);
-        else tma_load_2d_local(a_dst, ma, &full[s], k0, row_t);
-        if (g.b_mn) tma_load_2d_local(a_dst + kTOperand, mb, &full[s], col_t, k0);
-        else tma_load_2d_local(a_dst + kTOperand, mb, &full[s], k0, col_t);
-        ++issued;
+      for (; issued < nkb; ++issued) {
+        if (!bar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag)) { ok = false; break; }
+        expect_tx_at(full0 + 8 * stage, kTStageBytes);
+        const uint32_t a_dst = ring + stage * kTStageBytes;
+        tma_load_2d_local(a_dst, ma, &full[stage], ax, ay);
+        tma_load_2d_local(a_dst + kTOperand, mb, &full[stage], bx, by);
+        ax += adx; ay += ady; bx += bdx; by += bdy;
+        if (++stage == kTStages) { stage = 0; phase ^= 1u; }
       }
       if (!ok) give_up();
       // every copy has landed before the ring's space is used again or the CTA exits
@@ -171,53 +173,65 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
         (void)mbar_wait(&full[i % kTStages], (uint32_t)((i / kTStages) & 1), nullptr);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc = f8_idesc(g.a_e5m2, g.b_e5m2, g.a_mn, g.b_mn, kT, kT);
-      const uint32_t a_step = g.a_mn ? 4096 : 32, b_step = g.b_mn ? 4096 : 32;
+      const uint32_t a_step = (g.a_mn ? 4096 : 32) >> 4, b_step = (g.b_mn ? 4096 : 32) >> 4;
+      const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
+      const uint32_t sf_full0 = smem_u32(sf_full), sf_empty0 = smem_u32(sf_empty);
+      const uint64_t ring_desc = sdesc(smem_u32(smem), 16, 1024);
+      const uint64_t sf_desc = f8_sf_desc(smem_u32(sf_smem));
+      uint32_t stage = 0, phase = 0, set = 0, sf_phase = 0, accumulate = 0;
       bool ok = true;
-      for (int i = 0; i < nkb; ++i) {
-        const int s = i % kTStages, q = i % kF8Group, set = (i / kF8Group) % kTSfSets;
-        const uint32_t sfa = tmem + kTSfCol + set * 8, sfb = sfa + 4;
-        if (q == 0) {
-          if (!mbar_wait(&sf_full[set], (uint32_t)((i / (kF8Group * kTSfSets)) & 1), abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t src = smem_u32(sf_smem + set * kTSfSetBytes);
-          f8_copy_sf(sfa, f8_sf_desc(src));
-          f8_copy_sf(sfb, f8_sf_desc(src + kF8SfBytes));
-        }
-        if (!mbar_wait(&full[s], (uint32_t)((i / kTStages) & 1), abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t a_addr = smem_u32(smem + s * kTStageBytes), b_addr = a_addr + kTOperand;
-        const uint32_t id = f8_idesc_sf(idesc, q);
+      for (int kb = 0; kb < nkb && ok; kb += kF8Group) {
+        // copies and products run in the order of their issue, so the two sets in tensor memory
+        // need no barrier of their own
+        const uint32_t sfa = tmem + kTSfCol + (set & 1u) * 8, sfb = sfa + 4;
+        if (!bar_wait(sf_full0 + 8 * set, sf_phase, abort_flag)) { ok = false; break; }
+        const uint64_t src = sf_desc + (uint64_t)(set * (kTSfSetBytes >> 4));
+        f8_copy_sf(sfa, src);
+        f8_copy_sf(sfb, src + (kF8SfBytes >> 4));
+        const int n = min(kF8Group, nkb - kb);
+#pragma unroll 1
+        for (int q = 0; q < n; ++q) {
+          if (!bar_wait(full0 + 8 * stage, phase, abort_flag)) { ok = false; break; }
+          const uint64_t ad = ring_desc + (uint64_t)(stage * (kTStageBytes >> 4)), bd = ad + (kTOperand >> 4);
+          const uint32_t id = f8_idesc_sf(idesc, q);
+          f8_mma(tmem, ad, bd, id, sfa, sfb, accumulate);
+          accumulate = 1;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          f8_mma(tmem, sdesc(a_addr + k * a_step, 16, 1024), sdesc(b_addr + k * b_step, 16, 1024), id, sfa, sfb,
-                 (i > 0 || k > 0) ? 1u : 0u);
-        f8_commit(&empty[s]);
-        if (q == kF8Group - 1) f8_commit(&sf_empty[set]);
+          for (int k = 1; k < 4; ++k) f8_mma(tmem, ad + k * a_step, bd + k * b_step, id, sfa, sfb, 1u);
+          f8_commit_at(empty0 + 8 * stage);
+          if (++stage == kTStages) { stage = 0; phase ^= 1u; }
+        }
+        f8_commit_at(sf_empty0 + 8 * set);
+        if (++set == kTSfSets) { set = 0; sf_phase ^= 1u; }
       }
       if (!ok) give_up();
       f8_commit(done);
       (void)mbar_wait(done, 0, nullptr);  // every MMA and copy issued here is complete
     }
-  } else if (warp == 2) {
+  } else if (warp < 4) {
+    // warps 2 and 3 take the groups of 512 codes in turn
     const int groups = (nkb + kF8Group - 1) / kF8Group;
-    for (int i = 0; i < groups; ++i) {
-      const int set = i % kTSfSets;
+    uint32_t set = warp - 2, phase = 1;
+    for (int i = warp - 2; i < groups; i += 2) {
+      const int kb = kb_begin + i * kF8Group;
+      const uint4 wa = f8_sf_words(g.sa, row_t, g.m, kb, nkb_all, lane);
+      const uint4 wb = f8_sf_words(g.sb, col_t, g.n, kb, nkb_all, lane);
       int ok = 1;
-      if (lane == 0) ok = mbar_wait(&sf_empty[set], (uint32_t)((i / kTSfSets) & 1) ^ 1u, abort_flag);
+      if (lane == 0) ok = mbar_wait(&sf_empty[set], phase, abort_flag);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) {
         if (lane == 0) give_up();
         break;
       }
       uint8_t* dst = sf_smem + set * kTSfSetBytes + lane * 16;
-      const int kb = kb_begin + i * kF8Group;
-      *reinterpret_cast<uint4*>(dst) = f8_sf_words(g.sa, row_t, g.m, kb, nkb_all, lane);
-      *reinterpret_cast<uint4*>(dst + kF8SfBytes) = f8_sf_words(g.sb, col_t, g.n, kb, nkb_all, lane);
+      *reinterpret_cast<uint4*>(dst) = wa;
+      *reinterpret_cast<uint4*>(dst + kF8SfBytes) = wb;
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&sf_full[set])) : "memory");
+      if (lane == 0) mbar_arrive(&sf_full[set]);
+      if ((set += 2) >= kTSfSets) { set = warp - 2; phase ^= 1u; }
     }
   }
 

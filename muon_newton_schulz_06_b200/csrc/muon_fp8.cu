@@ -1,6 +1,7 @@
 // Host side of the 8-bit operators: argument checks, kernel parameters and tensor maps,
 // launches.  Nothing is kept between calls but the handle's status word.
 #include <algorithm>
+#include <cstdlib>
 #include <vector>
 
 #include <nvtx3/nvToolsExt.h>
@@ -278,52 +279,137 @@ int choose_split(int64_t tiles, int64_t kb, int sm_count) {
   return split;
 }
 
-// The products products[live[..]], at most N per launch.
+// The results' tensor map of the pair kernel: boxes of 32 rows x 64 bytes.
+muon_status encode_result(muon_handle* h, CUtensorMap* map, void* base, int64_t rows, int64_t cols, int64_t ld,
+                          int out) {
+  const CUtensorMapDataType type = out == kF8OutBf16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                   : out == kF8OutF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                                      : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const cuuint64_t esz = out == kF8OutBf16 ? 2 : out == kF8OutF32 ? 4 : 1;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)ld * esz};
+  cuuint32_t box[2] = {(cuuint32_t)(64 / esz), 32};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r =
+      h->encode(map, type, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(h, MUON_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return MUON_OK;
+}
+
+struct ProductSize {
+  int32_t m, n, k;
+};
+ProductSize size_of(const muon_fp8_product& q) {
+  return {(int32_t)(q.trans_a ? q.a.cols : q.a.rows), (int32_t)(q.trans_b ? q.b.rows : q.b.cols),
+          (int32_t)(q.trans_a ? q.a.rows : q.a.cols)};
+}
+
+// Products [b, end) of `live` in one launch: tiles of `tile` rows and columns.
+template <typename Params>
+muon_status fill_products(muon_handle* h, Params& p, const muon_fp8_product* products, const int* live, int count,
+                          int tile, int64_t* total, int64_t* min_kb) {
+  p.n = 0;
+  p.backward = 0;
+  p.status = h->fp8_status_dev;
+  *total = 0;
+  *min_kb = INT64_MAX;
+  for (int i = 0; i < count; ++i) {
+    const muon_fp8_product& q = products[live[i]];
+    const ProductSize sz = size_of(q);
+    F8Product g = {};
+    g.m = sz.m;
+    g.n = sz.n;
+    g.k = sz.k;
+    g.tiles_m = (g.m + tile - 1) / tile;
+    g.tiles_n = (g.n + tile - 1) / tile;
+    g.a_mn = q.trans_a ? 1 : 0;
+    g.b_mn = q.trans_b ? 0 : 1;
+    g.a_e5m2 = q.a.format == MUON_E5M2;
+    g.b_e5m2 = q.b.format == MUON_E5M2;
+    g.sa = scales_of(q.a, g.a_mn);
+    g.sb = scales_of(q.b, g.b_mn);
+    if (q.d.data) g.d = kernel_dense(q.d);
+    else g.d8 = kernel_fp8(q.d8);
+    g.out = !q.d.data ? kF8OutCodes : q.d.dtype == MUON_BF16 ? kF8OutBf16 : kF8OutF32;
+    if (q.c.data) g.c = kernel_dense(q.c);
+    g.epi = (int32_t)q.epilogue;
+    if (q.epilogue == MUON_EPI_RELU2_BACKWARD) {
+      g.saved = kernel_fp8(q.saved);
+      p.backward = 1;
+    }
+    g.tile_begin = (int32_t)*total;
+    *total += (int64_t)g.tiles_m * g.tiles_n;
+    *min_kb = std::min(*min_kb, blocks_of(g.k));
+    if (*total > INT32_MAX / 8) return fail(h, MUON_ERR_UNSUPPORTED, "item %d: the result has too many tiles", live[i]);
+    muon_status s;
+    if (g.k > 0 && ((s = encode_codes(h, &p.map_a[p.n], q.a)) || (s = encode_codes(h, &p.map_b[p.n], q.b)))) return s;
+    p.p[p.n++] = g;
+  }
+  p.total_tiles = (int)*total;
+  return MUON_OK;
+}
+
 template <int N>
+muon_status launch_pair_products(muon_handle* h, const muon_fp8_product* products, const int* live, int count,
+                                 cudaStream_t st) {
+  F8PairParamsN<N> p;
+  int64_t tiles = 0, min_kb = 0;
+  muon_status s = fill_products(h, p, products, live, count, kF8PairTile, &tiles, &min_kb);
+  if (s) return s;
+  for (int i = 0; i < count; ++i) {
+    const F8Product& g = p.p[i];
+    if (g.out == kF8OutCodes) s = encode_result(h, &p.map_d[i], g.d8.codes, g.m, g.n, g.d8.ld, g.out);
+    else if (g.d.vec) s = encode_result(h, &p.map_d[i], g.d.data, g.m, g.n, g.d.ld, g.out);
+    if (s) return s;
+  }
+  prof_begin(h, st, kFp8KindBase + MUON_FP8_KIND_MATMUL);
+  const cudaError_t e = launch_fp8_gemm_pair(p, (int)std::min<int64_t>(tiles, h->sm_count / 2), st);
+  prof_end(h, kFp8KindBase + MUON_FP8_KIND_MATMUL, st);
+  if (e != cudaSuccess) return cuda_fail(h, e, "8-bit product launch");
+  h->last_launches++;
+  return MUON_OK;
+}
+
+template <int N>
+muon_status launch_tile_products(muon_handle* h, const muon_fp8_product* products, const int* live, int count,
+                                 cudaStream_t st) {
+  F8GemmParamsN<N> p;
+  int64_t tiles = 0, min_kb = 0;
+  const muon_status s = fill_products(h, p, products, live, count, kFp8Block, &tiles, &min_kb);
+  if (s) return s;
+  prof_begin(h, st, kFp8KindBase + MUON_FP8_KIND_MATMUL);
+  const cudaError_t e = launch_fp8_gemm_tile(p, choose_split(tiles, min_kb, h->sm_count), st);
+  prof_end(h, kFp8KindBase + MUON_FP8_KIND_MATMUL, st);
+  if (e != cudaSuccess) return cuda_fail(h, e, "8-bit product launch");
+  h->last_launches++;
+  return MUON_OK;
+}
+
+// The products products[live[..]], at most kMaxF8Products per launch.
 muon_status launch_products(muon_handle* h, const muon_fp8_product* products, const std::vector<int>& live,
                             cudaStream_t st) {
-  F8GemmParamsN<N> p;
-  p.status = h->fp8_status_dev;
   for (size_t b = 0; b < live.size();) {
-    int64_t tiles = 0, min_kb = INT64_MAX;
-    p.n = 0;
-    for (; b < live.size() && p.n < N; ++b) {
-      const muon_fp8_product& q = products[live[b]];
-      F8Product g = {};
-      g.m = (int32_t)(q.trans_a ? q.a.cols : q.a.rows);
-      g.k = (int32_t)(q.trans_a ? q.a.rows : q.a.cols);
-      g.n = (int32_t)(q.trans_b ? q.b.rows : q.b.cols);
-      g.tiles_m = (int32_t)blocks_of(g.m);
-      g.tiles_n = (int32_t)blocks_of(g.n);
-      const int64_t t = (int64_t)g.tiles_m * g.tiles_n;
-      if (t > INT32_MAX / 8) return fail(h, MUON_ERR_UNSUPPORTED, "item %d: the result has too many tiles", live[b]);
-      if (p.n > 0 && tiles + t > INT32_MAX / 8) break;
-      g.a_mn = q.trans_a ? 1 : 0;
-      g.b_mn = q.trans_b ? 0 : 1;
-      g.a_e5m2 = q.a.format == MUON_E5M2;
-      g.b_e5m2 = q.b.format == MUON_E5M2;
-      g.sa = scales_of(q.a, g.a_mn);
-      g.sb = scales_of(q.b, g.b_mn);
-      if (q.d.data) g.d = kernel_dense(q.d);
-      else g.d8 = kernel_fp8(q.d8);
-      if (q.c.data) g.c = kernel_dense(q.c);
-      g.epi = (int32_t)q.epilogue;
-      if (q.epilogue == MUON_EPI_RELU2_BACKWARD) g.saved = kernel_fp8(q.saved);
-      g.tile_begin = (int32_t)tiles;
-      muon_status s;
-      if (g.k > 0 && ((s = encode_codes(h, &p.map_a[p.n], q.a)) || (s = encode_codes(h, &p.map_b[p.n], q.b))))
-        return s;
-      p.p[p.n++] = g;
-      tiles += t;
-      min_kb = std::min(min_kb, blocks_of(g.k));
+    const int count = (int)std::min<size_t>(kMaxF8Products, live.size() - b);
+    int64_t pair_tiles = 0;
+    bool pair = true;
+    for (int i = 0; i < count; ++i) {
+      const ProductSize sz = size_of(products[live[b + i]]);
+      pair_tiles += ((int64_t)sz.m + kF8PairTile - 1) / kF8PairTile * ((sz.n + kF8PairTile - 1) / kF8PairTile);
+      pair = pair && sz.k > 0;
     }
-    p.total_tiles = (int)tiles;
-    const int split = choose_split(tiles, min_kb, h->sm_count);
-    prof_begin(h, st, kFp8KindBase + MUON_FP8_KIND_MATMUL);
-    const cudaError_t e = launch_fp8_gemm_tile(p, split, st);
-    prof_end(h, kFp8KindBase + MUON_FP8_KIND_MATMUL, st);
-    if (e != cudaSuccess) return cuda_fail(h, e, "8-bit product launch");
-    h->last_launches++;
+    static const int thr = getenv("F8PAIR") ? atoi(getenv("F8PAIR")) : 37;
+    pair = pair && pair_tiles >= thr;
+    const int* items = live.data() + b;
+    muon_status s;
+    if (pair)
+      s = count <= kF8FewProducts ? launch_pair_products<kF8FewProducts>(h, products, items, count, st)
+                                  : launch_pair_products<kMaxF8Products>(h, products, items, count, st);
+    else
+      s = count <= kF8FewProducts ? launch_tile_products<kF8FewProducts>(h, products, items, count, st)
+                                  : launch_tile_products<kMaxF8Products>(h, products, items, count, st);
+    if (s) return s;
+    b += (size_t)count;
   }
   return MUON_OK;
 }
@@ -484,9 +570,7 @@ muon_status muon_fp8_matmul(muon_handle_t h, const muon_fp8_product* products, i
   if ((s = ensure_fp8(h))) return s;
   if ((s = poll_status(h, false))) return s;
   h->last_launches = 0;
-  s = live.size() <= kF8FewProducts ? launch_products<kF8FewProducts>(h, products, live, st)
-                                    : launch_products<kMaxF8Products>(h, products, live, st);
-  if (s) return s;
+  if ((s = launch_products(h, products, live, st))) return s;
   return finish_fp8(h, st);
 }
 
