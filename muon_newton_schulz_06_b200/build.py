@@ -34,7 +34,7 @@ def build(verbose_ptxas=False, force=False):
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
     cmd = [nvcc, *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
-           "-Xcompiler", "-fvisibility=hidden", "-cudart", "static",
+           "-Xcompiler", "-fvisibility=hidden", "-cudart", "static", "--threads", "0",
            "-I", os.path.join(ROOT, "include"), "-o", LIB + ".tmp", *sources()]
     if verbose_ptxas:
         cmd[1:1] = ["-Xptxas", "-v"]

@@ -43,7 +43,11 @@ __device__ __forceinline__ float f8_finite_abs(float v) {
 }
 
 // f(u) = max(u, 0)^2; NaN stays NaN.
-__device__ __forceinline__ float f8_relu2(float u) { return u > 0.f ? __fmul_rn(u, u) : (u == u ? 0.f : u); }
+__device__ __forceinline__ float f8_relu2(float u) {
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(u));
+  return __fmul_rn(r, r);
+}
 // f'(u) = 2 relu(u) = 2 sqrt(h) from h = f(u) = q 2^e: with p the parity of e,
 // 2 sqrt(q 2^p) 2^((e - p) / 2), whose power of two is exact.  The first factor is one of 512
 // numbers (code, parity), kept in shared memory: a lookup and a product per entry in the

@@ -73,7 +73,7 @@ struct F8Scales {
 
 enum F8Epi : int { kF8EpiNone = 0, kF8EpiRelu2 = 1, kF8EpiRelu2Backward = 2 };
 
-// How a result leaves the pair kernel (boxes of 32 rows x 64 bytes).
+// How a result leaves the pair kernel.
 enum F8Out : int { kF8OutBf16 = 0, kF8OutF32 = 1, kF8OutCodes = 2 };
 
 struct F8Product {
@@ -84,7 +84,8 @@ struct F8Product {
   uint8_t a_mn, b_mn;      // operand stored with M / N contiguous (contraction over its rows)
   uint8_t a_e5m2, b_e5m2;
   int32_t epi;
-  int32_t out;             // F8Out (pair kernel)
+  int32_t out;             // F8Out
+  int32_t out_align;       // largest of 32, 16 that divides the result's base and row pitch in bytes, else 0
   int32_t tiles_m, tiles_n;
   int32_t tile_begin;      // first tile inside the launch
 };
@@ -103,19 +104,10 @@ struct __align__(64) F8GemmParamsN {
 static_assert(sizeof(F8GemmParamsN<kMaxF8Products>) <= 32764,
               "parameters of the 8-bit products must fit the kernel parameter space");
 
-// The pair kernel's parameters: the same with a tensor map of each result (not used for a
-// dense result whose rows are not 16-byte aligned).
-constexpr int kF8PairTile = 256;
-template <int N>
-struct __align__(64) F8PairParamsN : F8GemmParamsN<N> {
-  CUtensorMap map_d[N];
-};
-static_assert(sizeof(F8PairParamsN<kMaxF8Products>) <= 32764,
-              "parameters of the 8-bit products must fit the kernel parameter space");
-
 // 256 x 256 tiles by pairs of CTAs, persistent: `clusters` pairs.
-cudaError_t launch_fp8_gemm_pair(const F8PairParamsN<kF8FewProducts>& p, int clusters, cudaStream_t st);
-cudaError_t launch_fp8_gemm_pair(const F8PairParamsN<kMaxF8Products>& p, int clusters, cudaStream_t st);
+constexpr int kF8PairTile = 256;
+constexpr int kF8PairProducts = 8;
+cudaError_t launch_fp8_gemm_pair(const F8GemmParamsN<kF8PairProducts>& p, int clusters, cudaStream_t st);
 
 // 128 x 128 tiles, one CTA each; `split` CTAs (a cluster: 1, 2, 4 or 8) share a tile's
 // contraction and join their sums through distributed shared memory.

@@ -14,8 +14,8 @@
 //   warps 2, 3   scale words: this CTA's 128 rows of A, all 256 columns of B, per 512 codes
 //   warps 4..11  epilogue of this CTA's 128 x 256 half, two warps per lane quadrant, each with
 //                a 128 x 128 block's worth of columns: exactly one scale block of an 8-bit
-//                result.  Results leave through 2 KB of shared memory per warp (32 rows x 64
-//                bytes, 64-byte swizzle) and TMA stores.
+//                result.  A thread holds 32 consecutive entries of a row and stores them as
+//                whole 32-byte sectors.
 //
 // Tensor memory holds two accumulators that share 32 columns, [0, 256) and [224, 480), and two
 // sets of scales in the rest: 512 columns have no room for two whole accumulators and scales.
@@ -24,6 +24,7 @@
 //
 // An 8-bit result needs its block's maximum before the first code: the four warps of a block
 // read the accumulator twice (maximum; codes), keeping only the shared columns in registers.
+// What took lookups or loads in the first reading is written back to tensor memory.
 // Every wait is bounded, the exchange of the maxima included.
 #include <atomic>
 
@@ -41,7 +42,7 @@ constexpr uint32_t kPStage = 2 * kPOperand;
 constexpr uint32_t kPairTx = 2 * kPStage;
 constexpr uint32_t kPSfSet = 3 * kF8SfBytes;          // A words, B words of both halves
 constexpr int kPSfSets = 4;                           // in shared memory
-constexpr uint32_t kOutStage = 2048;                  // 32 rows x 64 bytes per epilogue warp
+constexpr uint32_t kOutStage = 1024;                  // 32 rows x 32 bytes per epilogue warp (unaligned rows)
 constexpr uint32_t kPSmem =
     kPStages8 * kPStage + kEpi * kOutStage + kPSfSets * kPSfSet + 2 * kF8SlopeTable * 4 + 512 + 1024;
 static_assert(kPSmem <= 232448, "shared memory per CTA");
@@ -73,48 +74,87 @@ __device__ __forceinline__ PairTile pair_tile(const Params& p, int t) {
   return r;
 }
 
-// 32 consecutive entries of one row of the addend.
-__device__ __forceinline__ void add_c32(const F8Dense& c, int row, int col, int cols, float* v) {
-  const int64_t at = (int64_t)row * c.ld + col;
-  if (c.vec && col + 32 <= cols) {
-    if (c.bf16) {
-      const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(c.data) + at);
+// 32 bytes to an address that is 32-byte aligned: one whole sector.
+__device__ __forceinline__ void st_global_32b(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// Rows that 16-byte accesses cannot address (and blocks that end inside 16 bytes) go through a
+// warp's block in shared memory, 32 rows of 32 bytes, two bytes per lane and two rows at a
+// time.  Calls, so that the epilogue's loop stays small: with these inlined at every use the
+// kernel had 260 KB of code and the epilogue ran at the speed of instruction fetch (18,000
+// clocks per tile of 8-bit results in the place of 6,000).
+__device__ __noinline__ void rows_from_block(const uint8_t* blk, uint8_t* dst, int64_t pitch, int valid, int rows) {
+  const int lane = threadIdx.x & 31, off = 2 * (lane & 15);
+  __syncwarp();
+  for (int r = lane >> 4; r < rows; r += 2) {
+    const uint16_t x = *reinterpret_cast<const uint16_t*>(blk + r * 32 + ((off & 16) ^ ((r & 4) << 2)) + (off & 15));
+    uint8_t* d = dst + r * pitch + off;
+    if (off + 2 <= valid) *reinterpret_cast<uint16_t*>(d) = x;
+    else if (off < valid) *d = (uint8_t)x;
+  }
+  __syncwarp();
+}
+__device__ __noinline__ void rows_to_block(uint8_t* blk, const uint8_t* src, int64_t pitch, int valid, int rows) {
+  const int lane = threadIdx.x & 31, off = 2 * (lane & 15);
+  __syncwarp();
+  for (int r = lane >> 4; r < 32; r += 2)
+    *reinterpret_cast<uint16_t*>(blk + r * 32 + ((off & 16) ^ ((r & 4) << 2)) + (off & 15)) =
+        r < rows && off + 2 <= valid ? *reinterpret_cast<const uint16_t*>(src + r * pitch + off) : (uint16_t)0;
+  __syncwarp();
+}
+// 16 bytes q (0, 1) of row `lane` of such a block.
+__device__ __forceinline__ uint4* block16(uint8_t* blk, int lane, int q) {
+  return reinterpret_cast<uint4*>(blk + lane * 32 + ((q << 4) ^ ((lane & 4) << 2)));
+}
+// Infinite values among 8, see f8_encode_inf8.
+__device__ __noinline__ uint2 encode_inf8(float4 a, float4 b, uint2 c, bool e5m2) {
+  const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  return e5m2 ? f8_encode_inf8<true>(v, c) : f8_encode_inf8<false>(v, c);
+}
+
+// 32 consecutive entries of this thread's row of the addend (row0 + lane, col ..).
+template <bool BF16>
+__device__ __forceinline__ void add_c32(const F8Dense& c, uint8_t* blk, int row0, int rows, int col, int cols,
+                                        float (&v)[32]) {
+  constexpr int kEsz = BF16 ? 2 : 4;
+  const int lane = threadIdx.x & 31;
+  const uint8_t* src = reinterpret_cast<const uint8_t*>(c.data) + ((int64_t)row0 * c.ld + col) * kEsz;
+  const int64_t pitch = c.ld * kEsz;
+  const bool live = row0 + lane < rows;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 x = q[i];
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[8 * i + 2 * j] += __uint_as_float(w[j] << 16);
-          v[8 * i + 2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
-        }
-      }
+  for (int i = 0; i < kEsz; ++i) {  // 32 bytes of every row at a time
+    const int valid = min(32, (cols - col) * kEsz - 32 * i);
+    if (valid <= 0) break;
+    uint4 x[2];
+    if (c.vec && valid == 32) {
+      const uint4* q = reinterpret_cast<const uint4*>(src + lane * pitch + 32 * i);
+      x[0] = live ? q[0] : make_uint4(0u, 0u, 0u, 0u);
+      x[1] = live ? q[1] : make_uint4(0u, 0u, 0u, 0u);
     } else {
-      const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(c.data) + at);
+      rows_to_block(blk, src + 32 * i, pitch, valid, rows - row0);
+      x[0] = *block16(blk, lane, 0);
+      x[1] = *block16(blk, lane, 1);
+      __syncwarp();
+    }
+    const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 x = q[i];
-        v[4 * i] += x.x;
-        v[4 * i + 1] += x.y;
-        v[4 * i + 2] += x.z;
-        v[4 * i + 3] += x.w;
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (BF16) {
+        v[16 * i + 2 * j] += __uint_as_float(w[j] << 16);
+        v[16 * i + 2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
+      } else {
+        v[8 * i + j] += __uint_as_float(w[j]);
       }
     }
-    return;
   }
-#pragma unroll
-  for (int j = 0; j < 32; ++j)
-    if (col + j < cols)
-      v[j] += c.bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(c.data)[at + j])
-                     : reinterpret_cast<const float*>(c.data)[at + j];
 }
 
-// Writes 16 bytes q of row `lane` of a staged block (64-byte swizzle).
-__device__ __forceinline__ void stage16(uint8_t* blk, int lane, int q, uint4 x) {
-  *reinterpret_cast<uint4*>(blk + lane * 64 + (((q ^ (lane >> 1)) & 3) << 4)) = x;
-}
-
-template <typename Params>
+// OUT, EPI, ADD: the launch's kind of result, epilogue and addend where every product has the
+// same, -1 otherwise (decided per tile).
+template <typename Params, int OUT, int EPI, int ADD>
 __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -337,17 +377,27 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       const int chunks = row0 < g.m ? max(0, min(4, (g.n - col0 + 31) / 32)) : 0;
       // the chunk in the columns shared with the other accumulator, -1 for the other block
       const int shared_c = acc == 0 ? (half == 1 ? 3 : -1) : (half == 0 ? 0 : -1);
-      const bool backward = g.epi == kF8EpiRelu2Backward;
 
-      // the checkpoint's 128 codes of this row, requested before the accumulator is waited for
-      uint4 sv[8];
+      const int out = OUT >= 0 ? OUT : g.out;
+      const bool codes_out = out == kF8OutCodes;
+      const int epi = EPI >= 0 ? EPI : g.epi;
+      const bool backward = epi == kF8EpiRelu2Backward;
+      const bool add = ADD >= 0 ? ADD != 0 : g.c.data != nullptr;
+      const int rot = shared_c == 3 ? 3 : 0;  // the shared chunk comes first
+
+      // the checkpoint's codes of this row, requested one chunk ahead
       float sv_scale = 0.f;
       const float* table = slope;
-      if (backward) {
-        const uint8_t* q = g.saved.codes + (int64_t)row * g.saved.ld + col0;
+      uint4 sv_next[2];
+      auto request_saved = [&](int c) {
+        const uint8_t* q = g.saved.codes + (int64_t)row * g.saved.ld + col0 + 32 * c;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          sv[i] = live && col0 + 16 * i < g.n ? *reinterpret_cast<const uint4*>(q + 16 * i) : make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < 2; ++i)
+          sv_next[i] = live && col0 + 32 * c + 16 * i < g.n ? *reinterpret_cast<const uint4*>(q + 16 * i)
+                                                            : make_uint4(0u, 0u, 0u, 0u);
+      };
+      if (backward) {
+        request_saved(rot);
         const uint32_t sb = live && col0 < g.n ? *f8_scale_at(g.saved, row, col0 / kFp8Block) : 127u;
         const int e = (int)sb - 127, parity = e & 1;
         sv_scale = sb == 255u ? __uint_as_float(0x7fc00000u) : f8_exp2((e - parity) / 2);
@@ -357,205 +407,165 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       if (!warp_wait(&tfull[acc], (uint32_t)((it >> 1) & 1))) { ok = false; break; }
       tc_fence_after();
       const uint32_t tbase = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)acc * kAccStep + (uint32_t)(128 * half);
-
-      // chunk c (32 columns) with addend, activation or its gradient; columns past n are 0
-      auto finish = [&](int c, float* v) {
-        const int col = col0 + 32 * c;
-        if (g.c.data != nullptr && live) add_c32(g.c, row, col, g.n, v);
-        if (g.epi == kF8EpiRelu2) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = f8_relu2(v[j]);
-        } else if (backward) {
-          uint4 x[2];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i == c) { x[0] = sv[2 * i]; x[1] = sv[2 * i + 1]; }
-          const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            v[j] = __fmul_rn(__fmul_rn(table[(w[j >> 2] >> (8 * (j & 3))) & 255u], sv_scale), v[j]);
-        }
-        if (col + 32 > g.n) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (col + j >= g.n) v[j] = 0.f;
-        }
-      };
       auto release_shared = [&]() {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) remote_arrive(leader_tover + (uint32_t)(acc * sizeof(uint64_t)));
       };
-      // A warp's staged block (32 rows x 64 bytes) goes to column `col` of the result.  TMA
-      // stores clip at 16 bytes, not at an entry, so a block that ends inside 16 bytes of
-      // the result's last columns (and rows that TMA cannot address) is written by the warp,
-      // two bytes per lane.
-      auto stage_begin = [&]() {
-        if (lane == 0) bulk_wait_read_all();
-        __syncwarp();
-      };
-      const int esz = g.out == kF8OutBf16 ? 2 : g.out == kF8OutF32 ? 4 : 1;
-      const bool tma_ok = g.out == kF8OutCodes || g.d.vec;
-      auto stage_store = [&](int col) {
-        const int valid = min(64, (g.n - col) * esz);
-        if (tma_ok && (valid & 15) == 0) {
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d(&p.map_d[tl.gi], smem_u32(blk), col, row0);
-            bulk_commit();
-          }
-          return;
-        }
-        __syncwarp();
-        uint8_t* dst = g.out == kF8OutCodes ? g.d8.codes + (int64_t)row0 * g.d8.ld + col
-                                            : reinterpret_cast<uint8_t*>(g.d.data) + ((int64_t)row0 * g.d.ld + col) * esz;
-        const int64_t pitch = g.out == kF8OutCodes ? g.d8.ld : g.d.ld * esz;
-        const int off = 2 * lane;
-        for (int r = 0; r < 32 && row0 + r < g.m; ++r) {
-          const uint16_t x = *reinterpret_cast<const uint16_t*>(blk + r * 64 + ((((off >> 4) ^ (r >> 1)) & 3) << 4) + (off & 15));
-          uint8_t* d = dst + r * pitch + off;
-          if (off + 2 <= valid) *reinterpret_cast<uint16_t*>(d) = x;
-          else if (off < valid) *d = (uint8_t)x;
-        }
-        __syncwarp();
-      };
-
       if (shared_c >= 0 && shared_c >= chunks) release_shared();
-      if (g.out != kF8OutCodes) {
-        for (int k = 0; k < 4; ++k) {
-          const int c = shared_c == 3 ? (k + 3) & 3 : k;
-          if (c >= chunks) continue;
-          float v[32];
-          tmem_ld32(tbase + (uint32_t)(32 * c), v);
-          if (c == shared_c) release_shared();
-          finish(c, v);
-          const int col = col0 + 32 * c;
-          if (g.out == kF8OutBf16) {
-            stage_begin();
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint4 x;
-              __nv_bfloat162* hh = reinterpret_cast<__nv_bfloat162*>(&x);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) hh[e] = __floats2bfloat162_rn(v[8 * q + 2 * e], v[8 * q + 2 * e + 1]);
-              stage16(blk, lane, q, x);
-            }
-            stage_store(col);
-          } else {
-#pragma unroll
-            for (int hcol = 0; hcol < 2; ++hcol) {
-              if (col + 16 * hcol >= g.n) break;
-              stage_begin();
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                stage16(blk, lane, q,
-                        make_uint4(__float_as_uint(v[16 * hcol + 4 * q]), __float_as_uint(v[16 * hcol + 4 * q + 1]),
-                                   __float_as_uint(v[16 * hcol + 4 * q + 2]), __float_as_uint(v[16 * hcol + 4 * q + 3])));
-              stage_store(col + 16 * hcol);
-            }
-          }
+
+      // addend, activation or its gradient
+      auto finish = [&](int c, float (&v)[32]) {
+        const int col = col0 + 32 * c;
+        if (add) {
+          if (g.c.bf16) add_c32<true>(g.c, blk, row0, g.m, col, g.n, v);
+          else add_c32<false>(g.c, blk, row0, g.m, col, g.n, v);
         }
-      } else {
-        // first reading: the maximum; the shared chunk stays in registers, finished
-        float keep[32];
+        if (epi == kF8EpiRelu2) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = f8_relu2(v[j]);
+        } else if (backward) {
+          const uint32_t w[8] = {sv_next[0].x, sv_next[0].y, sv_next[0].z, sv_next[0].w,
+                                 sv_next[1].x, sv_next[1].y, sv_next[1].z, sv_next[1].w};
+          request_saved((c + 1) & 3);
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            v[j] = __fmul_rn(__fmul_rn(table[(w[j >> 2] >> (8 * (j & 3))) & 255u], sv_scale), v[j]);
+        }
+      };
+      // Steps of a tile: 8-bit results take 0 (largest magnitude), 1 (once more over finite
+      // entries, if some entry is infinite) and 2 (codes); dense ones step 2 alone.
+      const bool write_back = backward || add;
+      float keep[32];
+      float inv = 1.f;
+      bool any_inf = false;
+#pragma unroll 1
+      for (int step = codes_out ? 0 : 2; step < 3; ++step) {
+        if (step == 1 && !any_inf) continue;
         float vmax = 0.f;
+#pragma unroll 1
         for (int k = 0; k < 4; ++k) {
-          const int c = shared_c == 3 ? (k + 3) & 3 : k;
-          if (c >= chunks) continue;
+          const int c = (k + rot) & 3;
+          if (c >= chunks) {
+            if (backward && (step == 0 || !codes_out)) request_saved((c + 1) & 3);
+            continue;
+          }
+          const int col = col0 + 32 * c;
           float v[32];
+          // (the shared columns may hold the next tile's sums by now: `keep` replaces them)
           tmem_ld32(tbase + (uint32_t)(32 * c), v);
-          if (c == shared_c) release_shared();
-          finish(c, v);
-          if (live) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) vmax = fmaxf(vmax, fabsf(v[j]));
-          }
-          if (c == shared_c) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) keep[j] = v[j];
-          }
-        }
-        // value of chunk c again
-        auto again = [&](int c, float* v) {
-          if (c == shared_c) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = keep[j];
-          } else {
-            tmem_ld32(tbase + (uint32_t)(32 * c), v);
+          if (!codes_out) {
+            if (c == shared_c) release_shared();
             finish(c, v);
-          }
-        };
-        // maximum over the block: row blocks are this thread's own row
-        auto block_max = [&](float m, bool& good) {
-          if (g.d8.row_blocks) return m;
+          } else if (step == 0) {
+            if (c == shared_c) release_shared();
+            finish(c, v);
+            if (c == shared_c) {
 #pragma unroll
-          for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-          float* slot = max_slot + (max_turn & 1) * 8 + half * 4;
-          if (lane == 0) {
-            slot[quad] = m;
-            mbar_arrive(&max_bar[half]);
-          }
-          good = warp_wait(&max_bar[half], max_turn & 1u);
-          ++max_turn;
-          volatile float* s = slot;
-          return fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
-        };
-        bool good = true;
-        float amax = block_max(vmax, good);
-        if (!good) { ok = false; break; }
-        bool inf = amax == kF8Inf;
-        const bool any_inf = __any_sync(0xffffffffu, inf);
-        if (any_inf) {  // once more over finite entries
-          vmax = 0.f;
-          for (int c = 0; c < chunks; ++c) {
-            float v[32];
-            again(c, v);
-            if (live) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) vmax = fmaxf(vmax, f8_finite_abs(v[j]));
+              for (int j = 0; j < 32; ++j) keep[j] = v[j];
+            } else if (write_back) {
+              tmem_st32(tbase + (uint32_t)(32 * c), v);
             }
+          } else {
+            if (!write_back) finish(c, v);
+            const bool kept = c == shared_c;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = kept ? keep[j] : v[j];
           }
-          amax = block_max(vmax, good);
-          if (!good) { ok = false; break; }
-        }
-        const bool e5m2 = g.d8.e5m2;
-        const int e = f8_exponent(amax, e5m2);
-        const float inv = f8_exp2(-e);
-        if (g.d8.row_blocks) {
-          if (live && col0 < g.n) *f8_scale_at(g.d8, row, col0 / kFp8Block) = (uint8_t)(e + 127);
-        } else if (quad == 0 && lane == 0 && live && col0 < g.n) {
-          *f8_scale_at(g.d8, row, col0 / kFp8Block) = (uint8_t)(e + 127);
-        }
-        for (int c = 0; c < chunks; ++c) {
-          float v[32];
-          again(c, v);
-          if ((c & 1) == 0) stage_begin();
+          if (codes_out && step < 2) {
+            const int lim = live ? g.n - col : 0;  // columns that count
+            if (step == 0 && lim >= 32) {
+              float m4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint2 x[2];
+              for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], fabsf(v[j]));
+              vmax = fmaxf(vmax, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+            } else {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float* vv = v + 16 * q + 8 * i;
-              if (e5m2) {
-                x[i] = f8_encode8<true>(vv, inv);
-                if (any_inf) x[i] = f8_encode_inf8<true>(vv, x[i]);
-              } else {
-                x[i] = f8_encode8<false>(vv, inv);
-                if (any_inf) x[i] = f8_encode_inf8<false>(vv, x[i]);
+              for (int j = 0; j < 32; ++j)
+                vmax = fmaxf(vmax, j >= lim ? 0.f : step == 1 ? f8_finite_abs(v[j]) : fabsf(v[j]));
+            }
+            continue;
+          }
+          // 32 columns to the result, 32 bytes of a row at a time
+          const int parts = codes_out ? 1 : out == kF8OutBf16 ? 2 : 4;
+          uint8_t* const out0 = codes_out ? g.d8.codes : reinterpret_cast<uint8_t*>(g.d.data);
+          const int64_t pitch = codes_out ? g.d8.ld : 2 * (parts / 2) * g.d.ld;
+          uint8_t* const dst0 = out0 + row0 * pitch + (int64_t)col * parts;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i >= parts) break;
+            uint32_t w[8];
+            if (parts == 4) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * i + j]);
+            } else if (parts == 2) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const __nv_bfloat162 hh = __floats2bfloat162_rn(v[(16 * i + 2 * j) & 31], v[(16 * i + 2 * j + 1) & 31]);
+                w[j] = *reinterpret_cast<const uint32_t*>(&hh);
+              }
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                uint2 x;
+                if (g.d8.e5m2) x = f8_encode8<true>(v + 8 * q, inv);
+                else x = f8_encode8<false>(v + 8 * q, inv);
+                if (any_inf)
+                  x = encode_inf8(make_float4(v[8 * q], v[8 * q + 1], v[8 * q + 2], v[8 * q + 3]),
+                                  make_float4(v[8 * q + 4], v[8 * q + 5], v[8 * q + 6], v[8 * q + 7]), x, g.d8.e5m2);
+                w[2 * q] = x.x;
+                w[2 * q + 1] = x.y;
               }
             }
-            stage16(blk, lane, 2 * (c & 1) + q, make_uint4(x[0].x, x[0].y, x[1].x, x[1].y));
+            const int valid = min(32, (g.n - col) * parts - 32 * i);
+            if (valid <= 0) break;
+            if (valid == 32 && g.out_align >= 16) {
+              uint8_t* d = dst0 + lane * pitch + 32 * i;
+              if (live) {
+                if (g.out_align >= 32) {
+                  st_global_32b(d, w);
+                } else {
+                  reinterpret_cast<uint4*>(d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                  reinterpret_cast<uint4*>(d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+              }
+            } else {
+              *block16(blk, lane, 0) = make_uint4(w[0], w[1], w[2], w[3]);
+              *block16(blk, lane, 1) = make_uint4(w[4], w[5], w[6], w[7]);
+              rows_from_block(blk, dst0 + 32 * i, pitch, valid, min(32, g.m - row0));
+            }
           }
-          if ((c & 1) == 1 || c == chunks - 1) stage_store(col0 + 64 * (c >> 1));
+        }
+        if (step == 2) break;
+        // the block's maximum: over this thread's own row, or over the block's four warps
+        float amax = vmax;
+        if (!g.d8.row_blocks) {
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+          float* slot = max_slot + (max_turn & 1) * 8 + half * 4;
+          if (lane == 0) {
+            slot[quad] = amax;
+            mbar_arrive(&max_bar[half]);
+          }
+          if (!warp_wait(&max_bar[half], max_turn & 1u)) { ok = false; break; }
+          ++max_turn;
+          volatile float* sl = slot;
+          amax = fmaxf(fmaxf(sl[0], sl[1]), fmaxf(sl[2], sl[3]));
+        }
+        if (step == 0) any_inf = __any_sync(0xffffffffu, amax == kF8Inf);
+        if (step == 1 || !any_inf) {
+          const int e = f8_exponent(amax, g.d8.e5m2);
+          inv = f8_exp2(-e);
+          if (live && col0 < g.n && (g.d8.row_blocks || (quad == 0 && lane == 0)))
+            *f8_scale_at(g.d8, row, col0 / kFp8Block) = (uint8_t)(e + 127);
         }
       }
+      if (!ok) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) remote_arrive(leader_tdone + (uint32_t)(acc * sizeof(uint64_t)));
     }
     if (!ok && lane == 0) give_up();
-    if (lane == 0) bulk_wait_all();  // this warp's stores are complete and its staging is free
   }
 
   // both CTAs' MMAs, copies and stores are complete before either frees tensor memory or exits
@@ -568,16 +578,17 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
   }
 }
 
-template <typename Params>
-cudaError_t launch_pair(const Params& p, int clusters, cudaStream_t st) {
-  if (p.total_tiles == 0) return cudaSuccess;
+template <typename Params, int OUT, int EPI, int ADD>
+cudaError_t launch_variant(const Params& p, int clusters, cudaStream_t st) {
+  // once per device: the kernel's shared memory is above the default limit
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
   if (!(ready.load(std::memory_order_relaxed) & bit) || bit == 0) {
-    e = cudaFuncSetAttribute(fp8_pair_kernel<Params>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPSmem);
+    e = cudaFuncSetAttribute(fp8_pair_kernel<Params, OUT, EPI, ADD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)kPSmem);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
@@ -593,16 +604,33 @@ cudaError_t launch_pair(const Params& p, int clusters, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fp8_pair_kernel<Params>, p);
+  return cudaLaunchKernelEx(&cfg, fp8_pair_kernel<Params, OUT, EPI, ADD>, p);
 }
 
 }  // namespace
 
-cudaError_t launch_fp8_gemm_pair(const F8PairParamsN<kF8FewProducts>& p, int clusters, cudaStream_t st) {
-  return launch_pair(p, clusters, st);
-}
-cudaError_t launch_fp8_gemm_pair(const F8PairParamsN<kMaxF8Products>& p, int clusters, cudaStream_t st) {
-  return launch_pair(p, clusters, st);
+// The kinds of products that training steps issue have kernels of their own; the rest, and
+// launches that mix kinds, take the one that decides per tile.
+cudaError_t launch_fp8_gemm_pair(const F8GemmParamsN<kF8PairProducts>& p, int clusters, cudaStream_t st) {
+  using P = F8GemmParamsN<kF8PairProducts>;
+  if (p.total_tiles == 0) return cudaSuccess;
+  const F8Product& g = p.p[0];
+  const bool add = g.c.data != nullptr;
+  bool same = true;
+  for (int i = 1; i < p.n; ++i)
+    same = same && p.p[i].out == g.out && p.p[i].epi == g.epi && (p.p[i].c.data != nullptr) == add;
+  if (same && g.epi == kF8EpiNone && g.out == kF8OutBf16)
+    return add ? launch_variant<P, kF8OutBf16, kF8EpiNone, 1>(p, clusters, st)
+               : launch_variant<P, kF8OutBf16, kF8EpiNone, 0>(p, clusters, st);
+  if (same && g.epi == kF8EpiNone && g.out == kF8OutF32)
+    return add ? launch_variant<P, kF8OutF32, kF8EpiNone, 1>(p, clusters, st)
+               : launch_variant<P, kF8OutF32, kF8EpiNone, 0>(p, clusters, st);
+  if (same && g.out == kF8OutCodes && !add) {
+    if (g.epi == kF8EpiNone) return launch_variant<P, kF8OutCodes, kF8EpiNone, 0>(p, clusters, st);
+    if (g.epi == kF8EpiRelu2) return launch_variant<P, kF8OutCodes, kF8EpiRelu2, 0>(p, clusters, st);
+    return launch_variant<P, kF8OutCodes, kF8EpiRelu2Backward, 0>(p, clusters, st);
+  }
+  return launch_variant<P, -1, -1, -1>(p, clusters, st);
 }
 
 }  // namespace muon

@@ -279,24 +279,6 @@ int choose_split(int64_t tiles, int64_t kb, int sm_count) {
   return split;
 }
 
-// The results' tensor map of the pair kernel: boxes of 32 rows x 64 bytes.
-muon_status encode_result(muon_handle* h, CUtensorMap* map, void* base, int64_t rows, int64_t cols, int64_t ld,
-                          int out) {
-  const CUtensorMapDataType type = out == kF8OutBf16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                   : out == kF8OutF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                                      : CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  const cuuint64_t esz = out == kF8OutBf16 ? 2 : out == kF8OutF32 ? 4 : 1;
-  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)ld * esz};
-  cuuint32_t box[2] = {(cuuint32_t)(64 / esz), 32};
-  cuuint32_t estr[2] = {1, 1};
-  const CUresult r =
-      h->encode(map, type, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(h, MUON_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
-  return MUON_OK;
-}
-
 struct ProductSize {
   int32_t m, n, k;
 };
@@ -332,6 +314,9 @@ muon_status fill_products(muon_handle* h, Params& p, const muon_fp8_product* pro
     if (q.d.data) g.d = kernel_dense(q.d);
     else g.d8 = kernel_fp8(q.d8);
     g.out = !q.d.data ? kF8OutCodes : q.d.dtype == MUON_BF16 ? kF8OutBf16 : kF8OutF32;
+    const uint64_t at = q.d.data ? (uintptr_t)q.d.data | (uint64_t)q.d.ld * (q.d.dtype == MUON_BF16 ? 2 : 4)
+                                 : (uintptr_t)q.d8.codes | (uint64_t)q.d8.ld;
+    g.out_align = at % 32 == 0 ? 32 : at % 16 == 0 ? 16 : 0;
     if (q.c.data) g.c = kernel_dense(q.c);
     g.epi = (int32_t)q.epilogue;
     if (q.epilogue == MUON_EPI_RELU2_BACKWARD) {
@@ -350,19 +335,12 @@ muon_status fill_products(muon_handle* h, Params& p, const muon_fp8_product* pro
   return MUON_OK;
 }
 
-template <int N>
 muon_status launch_pair_products(muon_handle* h, const muon_fp8_product* products, const int* live, int count,
                                  cudaStream_t st) {
-  F8PairParamsN<N> p;
+  F8GemmParamsN<kF8PairProducts> p;
   int64_t tiles = 0, min_kb = 0;
-  muon_status s = fill_products(h, p, products, live, count, kF8PairTile, &tiles, &min_kb);
+  const muon_status s = fill_products(h, p, products, live, count, kF8PairTile, &tiles, &min_kb);
   if (s) return s;
-  for (int i = 0; i < count; ++i) {
-    const F8Product& g = p.p[i];
-    if (g.out == kF8OutCodes) s = encode_result(h, &p.map_d[i], g.d8.codes, g.m, g.n, g.d8.ld, g.out);
-    else if (g.d.vec) s = encode_result(h, &p.map_d[i], g.d.data, g.m, g.n, g.d.ld, g.out);
-    if (s) return s;
-  }
   prof_begin(h, st, kFp8KindBase + MUON_FP8_KIND_MATMUL);
   const cudaError_t e = launch_fp8_gemm_pair(p, (int)std::min<int64_t>(tiles, h->sm_count / 2), st);
   prof_end(h, kFp8KindBase + MUON_FP8_KIND_MATMUL, st);
@@ -386,28 +364,27 @@ muon_status launch_tile_products(muon_handle* h, const muon_fp8_product* product
   return MUON_OK;
 }
 
-// The products products[live[..]], at most kMaxF8Products per launch.
+// The products products[live[..]], in launches of a few.
 muon_status launch_products(muon_handle* h, const muon_fp8_product* products, const std::vector<int>& live,
                             cudaStream_t st) {
+  static const int thr = getenv("F8PAIR") ? atoi(getenv("F8PAIR")) : 37;
   for (size_t b = 0; b < live.size();) {
-    const int count = (int)std::min<size_t>(kMaxF8Products, live.size() - b);
+    // a run of products of one kind of kernel
     int64_t pair_tiles = 0;
     bool pair = true;
-    for (int i = 0; i < count; ++i) {
+    const int few = (int)std::min<size_t>(kF8PairProducts, live.size() - b);
+    for (int i = 0; i < few; ++i) {
       const ProductSize sz = size_of(products[live[b + i]]);
       pair_tiles += ((int64_t)sz.m + kF8PairTile - 1) / kF8PairTile * ((sz.n + kF8PairTile - 1) / kF8PairTile);
       pair = pair && sz.k > 0;
     }
-    static const int thr = getenv("F8PAIR") ? atoi(getenv("F8PAIR")) : 37;
     pair = pair && pair_tiles >= thr;
+    const int count = pair ? few : (int)std::min<size_t>(kMaxF8Products, live.size() - b);
     const int* items = live.data() + b;
-    muon_status s;
-    if (pair)
-      s = count <= kF8FewProducts ? launch_pair_products<kF8FewProducts>(h, products, items, count, st)
-                                  : launch_pair_products<kMaxF8Products>(h, products, items, count, st);
-    else
-      s = count <= kF8FewProducts ? launch_tile_products<kF8FewProducts>(h, products, items, count, st)
-                                  : launch_tile_products<kMaxF8Products>(h, products, items, count, st);
+    const muon_status s =
+        pair ? launch_pair_products(h, products, items, count, st)
+             : count <= kF8FewProducts ? launch_tile_products<kF8FewProducts>(h, products, items, count, st)
+                                       : launch_tile_products<kMaxF8Products>(h, products, items, count, st);
     if (s) return s;
     b += (size_t)count;
   }
