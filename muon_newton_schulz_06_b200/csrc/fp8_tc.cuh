@@ -116,43 +116,38 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 // barrier that is already complete is inlined and takes shared-memory addresses, and only a
 // real wait is a call.  (Through the general mbar_wait, with descriptors built per
 // instruction, an iteration took 1050 clocks and the tensor cores waited for it.)
-// CLUSTER: acquire at cluster scope, for barriers that publish the other CTA's shared memory.
-template <bool CLUSTER>
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
-  if constexpr (CLUSTER)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
   return ok != 0;
 }
-template <bool CLUSTER>
+constexpr long long kF8WaitClocks = 4000000000ll;  // about 2 s at full clock
 __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  const uint64_t t0 = global_timer();
+  const long long t0 = clock64();
   uint32_t n = 0;
   while (true) {
-    if (bar_try<CLUSTER>(bar, parity)) return true;
+    if (bar_try(bar, parity)) return true;
     if ((++n & 63u) == 0) {
-      if (*abort_flag) return false;
-      if (global_timer() - t0 > kWaitLimitNs) return false;
+      if (abort_flag != nullptr && *abort_flag) return false;
+      if (clock64() - t0 > kF8WaitClocks) return false;
     }
   }
 }
-template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  return bar_try<CLUSTER>(bar, parity) || bar_wait_slow<CLUSTER>(bar, parity, abort_flag);
+  return bar_try(bar, parity) || bar_wait_slow(bar, parity, abort_flag);
+}
+
+// Arrives on a barrier of either CTA of the pair to hand over tensor memory that has been
+// read.  No release at cluster scope: that waits for the thread's global stores (1,200 clocks
+// in the epilogue), which the reader of this barrier does not look at.
+__device__ __forceinline__ void arrive_tmem_free(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // Commits by shared-memory address: on this CTA's barrier, or at the same offset in both CTAs.

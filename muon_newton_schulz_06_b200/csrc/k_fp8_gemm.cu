@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
       if (!ok) give_up();
       // every copy has landed before the ring's space is used again or the CTA exits
       for (int i = max(0, issued - kTStages); i < issued; ++i)
-        (void)mbar_wait(&full[i % kTStages], (uint32_t)((i / kTStages) & 1), nullptr);
+        (void)bar_wait(smem_u32(&full[i % kTStages]), (uint32_t)((i / kTStages) & 1), nullptr);
     }
   } else if (warp == 1) {
     if (elect_one()) {
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
       }
       if (!ok) give_up();
       f8_commit(done);
-      (void)mbar_wait(done, 0, nullptr);  // every MMA and copy issued here is complete
+      (void)bar_wait(smem_u32(done), 0, nullptr);  // every MMA and copy issued here is complete
     }
   } else if (warp < 4) {
     // warps 2 and 3 take the groups of 512 codes in turn
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
       const uint4 wa = f8_sf_words(g.sa, row_t, g.m, kb, nkb_all, lane);
       const uint4 wb = f8_sf_words(g.sb, col_t, g.n, kb, nkb_all, lane);
       int ok = 1;
-      if (lane == 0) ok = mbar_wait(&sf_empty[set], phase, abort_flag);
+      if (lane == 0) ok = bar_wait(smem_u32(&sf_empty[set]), phase, abort_flag);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) {
         if (lane == 0) give_up();

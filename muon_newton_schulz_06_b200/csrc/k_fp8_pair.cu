@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       } else if (rank == 0) {
         for (uint32_t s = 0; s < kPStages8; ++s) {
           const uint32_t par = (s < stage) ? phase : (phase ^ 1u);
-          (void)mbar_wait(&full[s], par, nullptr);
+          (void)bar_wait(smem_u32(&full[s]), par, nullptr);
         }
       }
     }
@@ -274,8 +274,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
         const int acc = it & 1;
         const uint32_t idesc = f8_idesc(g.a_e5m2, g.b_e5m2, g.a_mn, g.b_mn, kF8PairTile, kF8PairTile);
         const uint32_t a_step = (g.a_mn ? 4096 : 32) >> 4, b_step = (g.b_mn ? 4096 : 32) >> 4;
-        if (!mbar_wait(&tdone[acc], (uint32_t)((it >> 1) & 1) ^ 1u, abort_flag) ||
-            (it > 0 && !mbar_wait(&tover[acc ^ 1], (uint32_t)(((it - 1) >> 1) & 1), abort_flag))) {
+        if (!bar_wait(smem_u32(&tdone[acc]), (uint32_t)((it >> 1) & 1) ^ 1u, abort_flag) ||
+            (it > 0 && !bar_wait(smem_u32(&tover[acc ^ 1]), (uint32_t)(((it - 1) >> 1) & 1), abort_flag))) {
           ok = false;
           break;
         }
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
           // copies and products run in the order of their issue, so the two sets in tensor
           // memory need no barrier of their own
           const uint32_t sfa = tmem + kPSfCol + (set & 1u) * kPSfCols, sfb = sfa + 4;
-          if (!bar_wait<true>(sf_full0 + 8 * set, sf_phase, abort_flag)) { ok = false; break; }
+          if (!bar_wait(sf_full0 + 8 * set, sf_phase, abort_flag)) { ok = false; break; }
           const uint64_t src = sf_desc + (uint64_t)(set * (kPSfSet >> 4));
           f8_copy_sf_pair(sfa, src);
           f8_copy_sf_pair(sfb, src + (kF8SfBytes >> 4));
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       }
       if (!ok) give_up();
       umma_commit_local(drain);
-      (void)mbar_wait(drain, 0, nullptr);
+      (void)bar_wait(smem_u32(drain), 0, nullptr);
     }
   } else if (warp < 4) {
     // ------------------------------------------------------------------ scale words (both CTAs)
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
         const uint4 w0 = f8_sf_words(g.sb, tl.col, g.n, kb, tl.nkb, lane);
         const uint4 w1 = f8_sf_words(g.sb, tl.col + 128, g.n, kb, tl.nkb, lane);
         int got = 1;
-        if (lane == 0) got = mbar_wait(&sf_empty[set], phase, abort_flag);
+        if (lane == 0) got = bar_wait(smem_u32(&sf_empty[set]), phase, abort_flag);
         got = __shfl_sync(0xffffffffu, got, 0);
         if (!got) {
           if (lane == 0) give_up();
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
     // one lane waits, so that the warp stays together when a wait runs out
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
       int got = 1;
-      if (lane == 0) got = mbar_wait(bar, parity, abort_flag);
+      if (lane == 0) got = bar_wait(smem_u32(bar), parity, abort_flag);
       got = __shfl_sync(0xffffffffu, got, 0);
       __syncwarp();
       return got != 0;
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       auto release_shared = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) remote_arrive(leader_tover + (uint32_t)(acc * sizeof(uint64_t)));
+        if (lane == 0) arrive_tmem_free(leader_tover + (uint32_t)(acc * sizeof(uint64_t)));
       };
       if (shared_c >= 0 && shared_c >= chunks) release_shared();
 
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       if (!ok) break;
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) remote_arrive(leader_tdone + (uint32_t)(acc * sizeof(uint64_t)));
+      if (lane == 0) arrive_tmem_free(leader_tdone + (uint32_t)(acc * sizeof(uint64_t)));
     }
     if (!ok && lane == 0) give_up();
   }
