@@ -107,7 +107,10 @@ static_assert(sizeof(F8GemmParamsN<kMaxF8Products>) <= 32764,
 // 256 x 256 tiles by pairs of CTAs, persistent: `clusters` pairs.
 constexpr int kF8PairTile = 256;
 constexpr int kF8PairProducts = 8;
-cudaError_t launch_fp8_gemm_pair(const F8GemmParamsN<kF8PairProducts>& p, int clusters, cudaStream_t st);
+struct __align__(64) F8PairParams : F8GemmParamsN<kF8PairProducts> {
+  CUtensorMap map_saved[kF8PairProducts];  // checkpoints, boxes of 32 rows x 128 codes
+};
+cudaError_t launch_fp8_gemm_pair(const F8PairParams& p, int clusters, cudaStream_t st);
 
 // 128 x 128 tiles, one CTA each; `split` CTAs (a cluster: 1, 2, 4 or 8) share a tile's
 // contraction and join their sums through distributed shared memory.

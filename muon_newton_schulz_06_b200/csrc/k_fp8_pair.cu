@@ -23,8 +23,11 @@
 // then and overlap the rest of the epilogue.
 //
 // An 8-bit result needs its block's maximum before the first code: the four warps of a block
-// read the accumulator twice (maximum; codes), keeping only the shared columns in registers.
-// What took lookups or loads in the first reading is written back to tensor memory.
+// read the accumulator twice (maximum; codes). The shared columns wait in shared memory for the
+// second reading, the others in tensor memory, finished values in the place of sums. The
+// backward epilogue's checkpoint block comes by TMA, requested a tile ahead (its lookups took
+// 132 us per 8192 x 6144 x 1536 product with loads one chunk ahead and the shared columns in
+// registers).
 // Every wait is bounded, the exchange of the maxima included.
 #include <atomic>
 
@@ -34,7 +37,6 @@
 namespace muon {
 namespace {
 
-constexpr int kPStages8 = 6;
 constexpr int kEpi = 8;
 constexpr int kPairThreads = 128 + 32 * kEpi;
 constexpr uint32_t kPOperand = 128 * kF8K;            // 16 KB
@@ -43,9 +45,25 @@ constexpr uint32_t kPairTx = 2 * kPStage;
 constexpr uint32_t kPSfSet = 3 * kF8SfBytes;          // A words, B words of both halves
 constexpr int kPSfSets = 4;                           // in shared memory
 constexpr uint32_t kOutStage = 1024;                  // 32 rows x 32 bytes per epilogue warp (unaligned rows)
-constexpr uint32_t kPSmem =
-    kPStages8 * kPStage + kEpi * kOutStage + kPSfSets * kPSfSet + 2 * kF8SlopeTable * 4 + 512 + 1024;
-static_assert(kPSmem <= 232448, "shared memory per CTA");
+constexpr uint32_t kKeep = 4096;                      // 32 x 32 fp32 of the shared columns, per lane quadrant
+constexpr uint32_t kSaved = 4096;                     // 32 x 128 codes of the checkpoint, per epilogue warp
+
+// Shared memory by kind of kernel (OUT, EPI as in the kernel, -1: decided per tile).
+template <int OUT, int EPI>
+struct PairSmem {
+  static constexpr bool kHasKeep = OUT == kF8OutCodes || OUT < 0;
+  static constexpr bool kHasSaved = EPI == kF8EpiRelu2Backward;
+  static constexpr int kTables = EPI == kF8EpiRelu2Backward ? 1 : EPI < 0 ? 2 : 0;  // e4m3, e5m2
+  static constexpr int kStages = kHasSaved || OUT < 0 ? 5 : 6;
+  static constexpr uint32_t saved = kStages * kPStage;
+  static constexpr uint32_t keep = saved + (kHasSaved ? kEpi * kSaved : 0);
+  static constexpr uint32_t out = keep + (kHasKeep ? 4 * kKeep : 0);
+  static constexpr uint32_t sf = out + kEpi * kOutStage;
+  static constexpr uint32_t slope = sf + kPSfSets * kPSfSet;
+  static constexpr uint32_t bars = slope + kTables * kF8SlopeTable * 4;
+  static constexpr uint32_t bytes = bars + 512 + 1024;
+  static_assert(bytes <= 232448, "shared memory per CTA");
+};
 constexpr uint32_t kAccStep = 224;  // first column of accumulator a: 224 a
 constexpr uint32_t kPSfCol = 480;
 constexpr uint32_t kPSfCols = 12;                     // per set in tensor memory, two sets
@@ -158,10 +176,11 @@ template <typename Params, int OUT, int EPI, int ADD>
 __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* out_smem = smem + kPStages8 * kPStage;
-  uint8_t* sf_smem = out_smem + kEpi * kOutStage;
-  float* slope = reinterpret_cast<float*>(sf_smem + kPSfSets * kPSfSet);  // e4m3's table, e5m2's
-  uint64_t* full = reinterpret_cast<uint64_t*>(slope + 2 * kF8SlopeTable);
+  using L = PairSmem<OUT, EPI>;
+  constexpr int kPStages8 = L::kStages;
+  uint8_t* sf_smem = smem + L::sf;
+  float* slope = reinterpret_cast<float*>(smem + L::slope);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bars);
   uint64_t* empty = full + kPStages8;
   uint64_t* sf_full = empty + kPStages8;
   uint64_t* sf_empty = sf_full + kPSfSets;
@@ -170,7 +189,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
   uint64_t* tover = tdone + 2;   // its columns shared with the other one have been read
   uint64_t* max_bar = tover + 2; // [2]: maxima of the two blocks
   uint64_t* drain = max_bar + 2;
-  float* max_slot = reinterpret_cast<float*>(drain + 1);   // [2 turns][2 blocks][4 warps]
+  uint64_t* saved_bar = drain + 1;  // [kEpi]
+  uint64_t* keep_bar = saved_bar + kEpi;  // [4]: a tile's use of a quadrant's kept columns is over
+  float* max_slot = reinterpret_cast<float*>(keep_bar + 4);   // [2 turns][2 blocks][4 warps]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(max_slot + 16);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -180,9 +201,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
   const int cluster = blockIdx.x >> 1;
   const int n_clusters = gridDim.x >> 1;
 
-  if (p.backward) {
+  if (L::kTables > 0 && p.backward) {
     f8_slope_init(slope, false, threadIdx.x, kPairThreads);
-    f8_slope_init(slope + kF8SlopeTable, true, threadIdx.x, kPairThreads);
+    if (L::kTables > 1) f8_slope_init(slope + kF8SlopeTable, true, threadIdx.x, kPairThreads);
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPStages8; ++s) {
@@ -199,6 +220,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       mbar_init(&tover[a], kEpi);  // one block's warps of both CTAs
       mbar_init(&max_bar[a], 4);
     }
+    for (int a = 0; a < kEpi; ++a) mbar_init(&saved_bar[a], 1);
+    for (int a = 0; a < 4; ++a) mbar_init(&keep_bar[a], 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -353,7 +376,20 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
     // ------------------------------------------------------------------ epilogue (both CTAs)
     const int ew = warp - 4;
     const int quad = warp & 3, half = ew >> 2;
-    uint8_t* blk = out_smem + ew * kOutStage;
+    uint8_t* blk = smem + L::out + ew * kOutStage;
+    uint8_t* keep = smem + L::keep + quad * kKeep;    // the two blocks' warps take turns, tile by tile
+    uint8_t* saved = smem + L::saved + ew * kSaved;
+    // the checkpoint's 32 rows x 128 codes of this warp's part of tile t
+    auto request_block = [&](int t) {
+      if (t < p.total_tiles && lane == 0) {
+        const PairTile tl = pair_tile(p, t);
+        fence_async_smem();
+        mbar_arrive_expect_tx(&saved_bar[ew], kSaved);
+        tma_load_2d_local(smem_u32(saved), &p.map_saved[tl.gi], &saved_bar[ew], tl.col + 128 * half,
+                          tl.row + (int)rank * 128 + 32 * quad);
+      }
+    };
+    if (L::kHasSaved) request_block(cluster);
     const uint32_t leader_tdone = peer_addr(smem_u32(&tdone[0]), 0);
     const uint32_t leader_tover = peer_addr(smem_u32(&tover[0]), 0);
     uint32_t max_turn = 0;
@@ -385,11 +421,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       const bool add = ADD >= 0 ? ADD != 0 : g.c.data != nullptr;
       const int rot = shared_c == 3 ? 3 : 0;  // the shared chunk comes first
 
-      // the checkpoint's codes of this row, requested one chunk ahead
+      // the checkpoint's codes of this row: in shared memory, or requested one chunk ahead
       float sv_scale = 0.f;
       const float* table = slope;
       uint4 sv_next[2];
       auto request_saved = [&](int c) {
+        if (L::kHasSaved) return;
         const uint8_t* q = g.saved.codes + (int64_t)row * g.saved.ld + col0 + 32 * c;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -401,10 +438,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
         const uint32_t sb = live && col0 < g.n ? *f8_scale_at(g.saved, row, col0 / kFp8Block) : 127u;
         const int e = (int)sb - 127, parity = e & 1;
         sv_scale = sb == 255u ? __uint_as_float(0x7fc00000u) : f8_exp2((e - parity) / 2);
-        table = slope + (g.saved.e5m2 ? kF8SlopeTable : 0) + 256 * parity;
+        table = slope + (L::kTables > 1 && g.saved.e5m2 ? kF8SlopeTable : 0) + 256 * parity;
       }
 
       if (!warp_wait(&tfull[acc], (uint32_t)((it >> 1) & 1))) { ok = false; break; }
+      if (L::kHasSaved && !warp_wait(&saved_bar[ew], (uint32_t)(it & 1))) { ok = false; break; }
       tc_fence_after();
       const uint32_t tbase = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)acc * kAccStep + (uint32_t)(128 * half);
       auto release_shared = [&]() {
@@ -425,6 +463,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = f8_relu2(v[j]);
         } else if (backward) {
+          if (L::kHasSaved) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              sv_next[i] = *reinterpret_cast<const uint4*>(saved + lane * 128 + (((2 * c + i) ^ (lane & 7)) << 4));
+          }
           const uint32_t w[8] = {sv_next[0].x, sv_next[0].y, sv_next[0].z, sv_next[0].w,
                                  sv_next[1].x, sv_next[1].y, sv_next[1].z, sv_next[1].w};
           request_saved((c + 1) & 3);
@@ -435,8 +478,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       };
       // Steps of a tile: 8-bit results take 0 (largest magnitude), 1 (once more over finite
       // entries, if some entry is infinite) and 2 (codes); dense ones step 2 alone.
-      const bool write_back = backward || add;
-      float keep[32];
+      const bool write_back = epi != kF8EpiNone || add;
       float inv = 1.f;
       bool any_inf = false;
 #pragma unroll 1
@@ -452,25 +494,32 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
           }
           const int col = col0 + 32 * c;
           float v[32];
-          // (the shared columns may hold the next tile's sums by now: `keep` replaces them)
-          tmem_ld32(tbase + (uint32_t)(32 * c), v);
           if (!codes_out) {
+            tmem_ld32(tbase + (uint32_t)(32 * c), v);
             if (c == shared_c) release_shared();
             finish(c, v);
           } else if (step == 0) {
+            tmem_ld32(tbase + (uint32_t)(32 * c), v);
             if (c == shared_c) release_shared();
             finish(c, v);
             if (c == shared_c) {
+              // the other block's warp of this quadrant used the space for the tile before
+              if (it > 0 && !warp_wait(&keep_bar[quad], (uint32_t)((it - 1) & 1))) { ok = false; break; }
 #pragma unroll
-              for (int j = 0; j < 32; ++j) keep[j] = v[j];
+              for (int q = 0; q < 8; ++q)
+                *reinterpret_cast<float4*>(keep + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                    make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
             } else if (write_back) {
               tmem_st32(tbase + (uint32_t)(32 * c), v);
             }
-          } else {
-            if (!write_back) finish(c, v);
-            const bool kept = c == shared_c;
+          } else if (c == shared_c) {  // the columns may hold the next tile's sums by now
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = kept ? keep[j] : v[j];
+            for (int q = 0; q < 8; ++q) {
+              const float4 x = *reinterpret_cast<const float4*>(keep + lane * 128 + ((q ^ (lane & 7)) << 4));
+              v[4 * q] = x.x; v[4 * q + 1] = x.y; v[4 * q + 2] = x.z; v[4 * q + 3] = x.w;
+            }
+          } else {
+            tmem_ld32(tbase + (uint32_t)(32 * c), v);
           }
           if (codes_out && step < 2) {
             const int lim = live ? g.n - col : 0;  // columns that count
@@ -536,6 +585,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
             }
           }
         }
+        if (!ok) break;
+        if (L::kHasSaved && step == 0) {  // every lane has read the checkpoint: the next tile's may come
+          __syncwarp();
+          request_block(t + n_clusters);
+        }
         if (step == 2) break;
         // the block's maximum: over this thread's own row, or over the block's four warps
         float amax = vmax;
@@ -563,9 +617,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       if (!ok) break;
       tc_fence_before();
       __syncwarp();
+      if (L::kHasKeep && half == 1 - acc && lane == 0) mbar_arrive(&keep_bar[quad]);
       if (lane == 0) arrive_tmem_free(leader_tdone + (uint32_t)(acc * sizeof(uint64_t)));
     }
-    if (!ok && lane == 0) give_up();
+    if (!ok && lane == 0) {
+      give_up();
+      if (L::kHasSaved) spin_ns(kAbortGraceNs);  // a requested block lands within microseconds
+    }
   }
 
   // both CTAs' MMAs, copies and stores are complete before either frees tensor memory or exits
@@ -588,14 +646,14 @@ cudaError_t launch_variant(const Params& p, int clusters, cudaStream_t st) {
   const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
   if (!(ready.load(std::memory_order_relaxed) & bit) || bit == 0) {
     e = cudaFuncSetAttribute(fp8_pair_kernel<Params, OUT, EPI, ADD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)kPSmem);
+                             (int)PairSmem<OUT, EPI>::bytes);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * clusters));
   cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = kPSmem;
+  cfg.dynamicSmemBytes = PairSmem<OUT, EPI>::bytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -611,8 +669,8 @@ cudaError_t launch_variant(const Params& p, int clusters, cudaStream_t st) {
 
 // The kinds of products that training steps issue have kernels of their own; the rest, and
 // launches that mix kinds, take the one that decides per tile.
-cudaError_t launch_fp8_gemm_pair(const F8GemmParamsN<kF8PairProducts>& p, int clusters, cudaStream_t st) {
-  using P = F8GemmParamsN<kF8PairProducts>;
+cudaError_t launch_fp8_gemm_pair(const F8PairParams& p, int clusters, cudaStream_t st) {
+  using P = F8PairParams;
   if (p.total_tiles == 0) return cudaSuccess;
   const F8Product& g = p.p[0];
   const bool add = g.c.data != nullptr;
@@ -628,7 +686,9 @@ cudaError_t launch_fp8_gemm_pair(const F8GemmParamsN<kF8PairProducts>& p, int cl
   if (same && g.out == kF8OutCodes && !add) {
     if (g.epi == kF8EpiNone) return launch_variant<P, kF8OutCodes, kF8EpiNone, 0>(p, clusters, st);
     if (g.epi == kF8EpiRelu2) return launch_variant<P, kF8OutCodes, kF8EpiRelu2, 0>(p, clusters, st);
-    return launch_variant<P, kF8OutCodes, kF8EpiRelu2Backward, 0>(p, clusters, st);
+    bool e4m3 = true;
+    for (int i = 0; i < p.n; ++i) e4m3 = e4m3 && !p.p[i].saved.e5m2;
+    if (e4m3) return launch_variant<P, kF8OutCodes, kF8EpiRelu2Backward, 0>(p, clusters, st);
   }
   return launch_variant<P, -1, -1, -1>(p, clusters, st);
 }

@@ -243,10 +243,10 @@ bool same_dense(const muon_dense& a, const muon_dense& b) {
 
 // ------------------------------------------------------------------ products
 
-muon_status encode_codes(muon_handle* h, CUtensorMap* map, const muon_fp8_matrix& x) {
+muon_status encode_codes(muon_handle* h, CUtensorMap* map, const muon_fp8_matrix& x, int box_rows = kFp8Block) {
   cuuint64_t dims[2] = {(cuuint64_t)x.cols, (cuuint64_t)x.rows};
   cuuint64_t strides[1] = {(cuuint64_t)x.ld};
-  cuuint32_t box[2] = {(cuuint32_t)kFp8Block, (cuuint32_t)kFp8Block};
+  cuuint32_t box[2] = {(cuuint32_t)kFp8Block, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
   const CUresult r = h->encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, x.codes, dims, strides, box, estr,
                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -337,10 +337,12 @@ muon_status fill_products(muon_handle* h, Params& p, const muon_fp8_product* pro
 
 muon_status launch_pair_products(muon_handle* h, const muon_fp8_product* products, const int* live, int count,
                                  cudaStream_t st) {
-  F8GemmParamsN<kF8PairProducts> p;
+  F8PairParams p;
   int64_t tiles = 0, min_kb = 0;
-  const muon_status s = fill_products(h, p, products, live, count, kF8PairTile, &tiles, &min_kb);
+  muon_status s = fill_products(h, p, products, live, count, kF8PairTile, &tiles, &min_kb);
   if (s) return s;
+  for (int i = 0; i < count; ++i)
+    if (p.p[i].epi == kF8EpiRelu2Backward && (s = encode_codes(h, &p.map_saved[i], products[live[i]].saved, 32))) return s;
   prof_begin(h, st, kFp8KindBase + MUON_FP8_KIND_MATMUL);
   const cudaError_t e = launch_fp8_gemm_pair(p, (int)std::min<int64_t>(tiles, h->sm_count / 2), st);
   prof_end(h, kFp8KindBase + MUON_FP8_KIND_MATMUL, st);
