@@ -447,14 +447,13 @@ def _fp8(m, name: str) -> muon_fp8_matrix:
 def _dense(t: torch.Tensor, name: str) -> muon_dense:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be a 2-D tensor")
-    (rows, cols), (ld, step) = t.shape, t.stride()
+    (rows, cols), (ld, step) = shape, t.stride()
     if step != 1 and cols > 1 and rows > 0:
         raise ValueError(f"{name} must have consecutive columns")
-    if rows <= 1:
-        ld = cols
-    return muon_dense(t.data_ptr(), rows, cols, ld, _dtype_code(t))
+    return muon_dense(t.data_ptr(), rows, cols, ld if rows > 1 else cols, _dtype_code(t))
 
 
 def _list(struct, items, convert, name):
@@ -465,9 +464,10 @@ def _list(struct, items, convert, name):
 
 
 def _activation(act: str) -> int:
-    if act not in ACTIVATIONS:
+    code = ACTIVATIONS.get(act)
+    if code is None:
         raise ValueError(f"unknown activation {act!r}; use one of {sorted(ACTIVATIONS)}")
-    return ACTIVATIONS[act]
+    return code
 
 
 def _same_length(names: str, first, *others) -> int:
@@ -487,7 +487,9 @@ def muon_fp8_quantize(handle, xs: Sequence[torch.Tensor], outs: Sequence[Fp8Matr
     if n == 0:
         return
     x, o = _list(muon_dense, xs, _dense, "x"), _list(muon_fp8_matrix, outs, _fp8, "out")
-    _check(load_library().muon_fp8_quantize(handle, x, o, n, act, _stream_ptr(stream, xs[0].device)), handle)
+    code = load_library().muon_fp8_quantize(handle, x, o, n, act, _stream_ptr(stream, outs[0].device))
+    if code:
+        _check(code, handle)
 
 
 def muon_fp8_dequantize(handle, xs: Sequence[Fp8Matrix], outs: Sequence[torch.Tensor], stream=None) -> None:
@@ -496,7 +498,9 @@ def muon_fp8_dequantize(handle, xs: Sequence[Fp8Matrix], outs: Sequence[torch.Te
     if n == 0:
         return
     x, o = _list(muon_fp8_matrix, xs, _fp8, "x"), _list(muon_dense, outs, _dense, "out")
-    _check(load_library().muon_fp8_dequantize(handle, x, o, n, _stream_ptr(stream, xs[0].device)), handle)
+    code = load_library().muon_fp8_dequantize(handle, x, o, n, _stream_ptr(stream, xs[0].device))
+    if code:
+        _check(code, handle)
 
 
 def muon_fp8_act_backward(handle, dys: Sequence[torch.Tensor], saved: Sequence[Fp8Matrix], dus: Sequence,
@@ -514,8 +518,9 @@ def muon_fp8_act_backward(handle, dys: Sequence[torch.Tensor], saved: Sequence[F
             du8[i] = t.c
         else:
             du[i] = _dense(t, "du")
-    _check(load_library().muon_fp8_act_backward(handle, dy, sv, du, du8, n, act, _stream_ptr(stream, dys[0].device)),
-           handle)
+    code = load_library().muon_fp8_act_backward(handle, dy, sv, du, du8, n, act, _stream_ptr(stream, saved[0].device))
+    if code:
+        _check(code, handle)
 
 
 def muon_fp8_matmul(handle, products: Sequence[Fp8Product], stream=None) -> None:
@@ -541,7 +546,9 @@ def muon_fp8_matmul(handle, products: Sequence[Fp8Product], stream=None) -> None
             raise ValueError("saved belongs to the relu2_backward epilogue, which needs it")
         if p.saved is not None:
             q.saved = _fp8(p.saved, "saved")
-    _check(load_library().muon_fp8_matmul(handle, arr, n, _stream_ptr(stream, products[0].a.device)), handle)
+    code = load_library().muon_fp8_matmul(handle, arr, n, _stream_ptr(stream, products[0].a.device))
+    if code:
+        _check(code, handle)
 
 
 def muon_fp8_profile_read(handle) -> dict:

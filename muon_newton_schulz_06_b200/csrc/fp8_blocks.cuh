@@ -16,6 +16,12 @@
 namespace muon {
 namespace {
 
+// See f8_launch: the next kernel may be set up from here on; and the wait for the one before.
+__device__ __forceinline__ void f8_grid_wait() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // 2^e as a float for e in [-127, 127].
 __device__ __forceinline__ float f8_exp2(int e) {
   return e == -127 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(e + 127) << 23);

@@ -6,9 +6,48 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace muon {
 
 constexpr int kFp8Block = 128;
+
+// Launch of one of these kernels: `cluster` CTAs per cluster, and its start may overlap the
+// end of the kernel before it on the stream (programmatic stream serialization).  Every
+// kernel here lets the next one start as soon as all its CTAs run, and touches memory only
+// after f8_grid_wait(), which returns when the kernel before has completed: chains of small
+// calls hide their launch and set-up behind each other.
+template <typename Params>
+cudaError_t f8_launch(void (*kernel)(Params), const Params& p, int grid, int block, uint32_t smem, int cluster,
+                      cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// Raises a kernel's shared-memory limit, once per device (`ready`: one bit each).
+inline cudaError_t f8_allow_smem(const void* kernel, uint32_t bytes, std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (bit != 0 && (ready.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // A dense operand of a kernel (null data: absent).
 struct F8Dense {

@@ -57,6 +57,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_pass_kernel(const __grid_cons
       __syncthreads();
     }
   }
+  f8_grid_wait();
 
   // entries outside the matrix are 0, and stay 0 through f and the gradient
   float v[kIter][8];
@@ -124,11 +125,10 @@ template <typename Params>
 cudaError_t launch(int op, const Params& p, cudaStream_t st) {
   if (p.total_blocks == 0) return cudaSuccess;
   switch (op) {
-    case kF8Quantize: fp8_pass_kernel<kF8Quantize><<<p.total_blocks, kThreads, 0, st>>>(p); break;
-    case kF8Dequantize: fp8_pass_kernel<kF8Dequantize><<<p.total_blocks, kThreads, 0, st>>>(p); break;
-    default: fp8_pass_kernel<kF8ActBackward><<<p.total_blocks, kThreads, 0, st>>>(p); break;
+    case kF8Quantize: return f8_launch(fp8_pass_kernel<kF8Quantize, Params>, p, p.total_blocks, kThreads, 0, 1, st);
+    case kF8Dequantize: return f8_launch(fp8_pass_kernel<kF8Dequantize, Params>, p, p.total_blocks, kThreads, 0, 1, st);
+    default: return f8_launch(fp8_pass_kernel<kF8ActBackward, Params>, p, p.total_blocks, kThreads, 0, 1, st);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace

@@ -21,8 +21,6 @@
 //
 // Every mbarrier wait is bounded; on expiry the kernel writes kDevTimeout to the status
 // word, lets its copies and MMAs drain, frees tensor memory and returns.
-#include <atomic>
-
 #include "fp8_blocks.cuh"
 #include "fp8_tc.cuh"
 
@@ -140,6 +138,7 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  f8_grid_wait();
 
   auto give_up = [&]() {
     *reinterpret_cast<volatile int*>(p.status) = kDevTimeout;  // page-locked host word
@@ -400,30 +399,10 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
 template <typename Params>
 cudaError_t launch_tile(const Params& p, int split, cudaStream_t st) {
   if (p.total_tiles == 0) return cudaSuccess;
-  // once per device: the kernel's shared memory is above the default limit
   static std::atomic<uint64_t> ready{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = f8_allow_smem(reinterpret_cast<const void*>(fp8_tile_kernel<Params>), kTSmem, ready);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-  if (!(ready.load(std::memory_order_relaxed) & bit) || bit == 0) {
-    e = cudaFuncSetAttribute(fp8_tile_kernel<Params>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTSmem);
-    if (e != cudaSuccess) return e;
-    ready.fetch_or(bit, std::memory_order_relaxed);
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.total_tiles * split));
-  cfg.blockDim = dim3(kTThreads);
-  cfg.dynamicSmemBytes = kTSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fp8_tile_kernel<Params>, p);
+  return f8_launch(fp8_tile_kernel<Params>, p, p.total_tiles * split, kTThreads, kTSmem, split, st);
 }
 
 }  // namespace

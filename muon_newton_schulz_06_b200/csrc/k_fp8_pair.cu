@@ -29,8 +29,6 @@
 // 132 us per 8192 x 6144 x 1536 product with loads one chunk ahead and the shared columns in
 // registers).
 // Every wait is bounded, the exchange of the maxima included.
-#include <atomic>
-
 #include "fp8_blocks.cuh"
 #include "fp8_tc.cuh"
 
@@ -236,6 +234,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  f8_grid_wait();
   const uint32_t peer_abort = peer_addr(smem_u32((const void*)abort_flag), rank ^ 1u);
   auto give_up = [&]() {
     *reinterpret_cast<volatile int*>(p.status) = kDevTimeout;  // page-locked host word
@@ -638,31 +637,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
 
 template <typename Params, int OUT, int EPI, int ADD>
 cudaError_t launch_variant(const Params& p, int clusters, cudaStream_t st) {
-  // once per device: the kernel's shared memory is above the default limit
+  const auto kernel = fp8_pair_kernel<Params, OUT, EPI, ADD>;
+  constexpr uint32_t kSmem = PairSmem<OUT, EPI>::bytes;
   static std::atomic<uint64_t> ready{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = f8_allow_smem(reinterpret_cast<const void*>(kernel), kSmem, ready);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-  if (!(ready.load(std::memory_order_relaxed) & bit) || bit == 0) {
-    e = cudaFuncSetAttribute(fp8_pair_kernel<Params, OUT, EPI, ADD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)PairSmem<OUT, EPI>::bytes);
-    if (e != cudaSuccess) return e;
-    ready.fetch_or(bit, std::memory_order_relaxed);
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * clusters));
-  cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = PairSmem<OUT, EPI>::bytes;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fp8_pair_kernel<Params, OUT, EPI, ADD>, p);
+  return f8_launch<Params>(kernel, p, 2 * clusters, kPairThreads, kSmem, 2, st);
 }
 
 }  // namespace

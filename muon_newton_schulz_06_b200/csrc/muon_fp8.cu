@@ -275,6 +275,8 @@ F8Scales scales_of(const muon_fp8_matrix& x, bool mn) {
 // (two CTAs each) and every CTA keeps at least two k-blocks.
 int choose_split(int64_t tiles, int64_t kb, int sm_count) {
   int split = 1;
+  static const int force = getenv("F8SPLIT") ? atoi(getenv("F8SPLIT")) : 0;
+  if (force) return force;
   while (split < 8 && tiles * split * 2 <= 2 * sm_count && kb >= 4 * split) split *= 2;
   return split;
 }
