@@ -137,6 +137,7 @@ struct __align__(64) F8GemmParamsN {
   F8Product p[N];
   int n;
   int total_tiles;
+  int stages;              // ring depth of k_fp8_gemm.cu: 6, or 3 for two CTAs per SM
   int backward;            // some product has the kF8EpiRelu2Backward epilogue
   int* status;
 };
@@ -151,7 +152,7 @@ struct __align__(64) F8PairParams : F8GemmParamsN<kF8PairProducts> {
 };
 cudaError_t launch_fp8_gemm_pair(const F8PairParams& p, int clusters, cudaStream_t st);
 
-// 128 x 128 tiles, one CTA each; `split` CTAs (a cluster: 1, 2, 4 or 8) share a tile's
+// 128 x 128 tiles, one CTA each; `split` CTAs (a cluster of 1, 2 or 4) share a tile's
 // contraction and join their sums through distributed shared memory.
 cudaError_t launch_fp8_gemm_tile(const F8GemmParamsN<kF8FewProducts>& p, int split, cudaStream_t st);
 cudaError_t launch_fp8_gemm_tile(const F8GemmParamsN<kMaxF8Products>& p, int split, cudaStream_t st);

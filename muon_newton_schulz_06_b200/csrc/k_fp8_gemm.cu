@@ -8,16 +8,20 @@
 // with its contraction along rows (MN-major): weight and input gradients read the same
 // 8-bit copies as the forward pass, untransposed.
 //
-// Tile kernel: one CTA per 128 x 128 tile of D, 256 threads:
-//   warp 0   TMA producer: 3-stage ring of 128 x 128 code tiles of A and B (16 KB each)
-//   warp 1   tensor memory, MMA issue (one thread)
+// This file: one 128 x 128 tile per CTA, for results of few tiles, where latency counts
+// (64 x 512 x 512: 5.3 us in a chain of calls, against 6.6 us by the persistent kernel of
+// k_fp8_pair.cu and 9.7 us by one 256 x 256 tile per pair, which was not kept).  256 threads:
+//   warp 0      TMA producer: ring of 128 x 128 code tiles of A and B (16 KB each)
+//   warp 1      tensor memory, MMA issue (one thread)
 //   warps 2, 3  scale words of both operands, one set per 512 codes, four sets in flight
-//   all      epilogue: the fp32 tile goes through shared memory (the ring's space), then
-//            half a warp per row finishes 8 columns per thread, as the block passes do
-// With few tiles, a cluster of 2, 4 or 8 CTAs splits a tile's contraction: every CTA
-// leaves its partial tile in its shared memory, and each finishes 1 / split of the rows,
-// adding the partial sums in rank order through distributed shared memory.  No workspace,
-// no atomics, one launch.
+//   all         epilogue: the fp32 tile goes through shared memory (the ring's space), then
+//               half a warp per row finishes 8 columns per thread, as the block passes do
+// With few tiles and a long contraction a cluster of 2 or 4 CTAs splits it: every CTA leaves
+// its partial tile in its shared memory, and each finishes its share of the rows, adding the
+// partial sums in rank order through distributed shared memory.  No workspace, no atomics,
+// one launch, the same sums every time (2048 x 512 x 16384: 30.8 us whole, 20.7 us split in
+// two; bound by the operands' way into shared memory, 128 bytes per clock at the tensor
+// rate against the 50 or so that arrive).
 //
 // Every mbarrier wait is bounded; on expiry the kernel writes kDevTimeout to the status
 // word, lets its copies and MMAs drain, frees tensor memory and returns.
@@ -27,19 +31,23 @@
 namespace muon {
 namespace {
 
-constexpr int kT = 128;  // tile rows and columns
+constexpr int kT = 128;  // rows of A and of B that a CTA holds
 constexpr int kTThreads = 256;
-constexpr int kTStages = 3;
-constexpr uint32_t kTOperand = kT * kF8K;              // 16 KB
+constexpr uint32_t kTOperand = kT * kF8K;  // 16 KB
 constexpr uint32_t kTStageBytes = 2 * kTOperand;
-constexpr int kTSfSets = 4;                            // in shared memory; two in tensor memory
-constexpr uint32_t kTSfSetBytes = 2 * kF8SfBytes;      // A words, B words
-constexpr int kTPitch = kT + 4;                        // floats per staged row
-constexpr uint32_t kTRing = kTStages * kTStageBytes;
-static_assert(kT * kTPitch * 4 <= kTRing, "the staged tile reuses the ring");
-constexpr uint32_t kTSmem = kTRing + kTSfSets * kTSfSetBytes + 256 + kF8SlopeTable * 4 + 1024;
-constexpr uint32_t kTTmemCols = 256;  // 128 accumulator columns, 2 x 8 columns of scales
+constexpr int kTMaxStages = 6;
+constexpr int kTSfSets = 4;  // in shared memory; two in tensor memory
+
+constexpr uint32_t kTSfSet = 2 * kF8SfBytes;   // A words, B words
+constexpr uint32_t kTTmemCols = 256;           // accumulator, then two sets of 8 columns of scales
 constexpr uint32_t kTSfCol = 128;
+constexpr int kTPitch = kT + 4;                // floats per staged row
+static_assert(kT * kTPitch * 4 <= 3 * (int)kTStageBytes, "the staged tile reuses the ring");
+constexpr uint32_t tile_smem(int stages) {
+  return (uint32_t)stages * kTStageBytes + kTSfSets * kTSfSet + kF8SlopeTable * 4 + 512 + 1024;
+}
+// one CTA of six stages per SM, or two of three
+static_assert(tile_smem(kTMaxStages) <= 232448 && 2 * (tile_smem(3) + 1024) <= 233472, "shared memory");
 
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t n;
@@ -83,21 +91,42 @@ __device__ __forceinline__ void f8_finish(const F8Product& g, const float* slope
   }
 }
 
+// Sum over a cluster's partial tiles, in rank order, of 8 columns at `addr` in each (all
+// loads are issued before the first addition).
+template <int S>
+__device__ __forceinline__ void fetch_split(uint32_t addr, float* v) {
+  float4 a[S], b[S];
+#pragma unroll
+  for (int r = 0; r < S; ++r) {
+    const uint32_t at = peer_addr(addr, (uint32_t)r);
+    a[r] = ld_cluster_f4(at);
+    b[r] = ld_cluster_f4(at + 16);
+  }
+  v[0] = a[0].x; v[1] = a[0].y; v[2] = a[0].z; v[3] = a[0].w;
+  v[4] = b[0].x; v[5] = b[0].y; v[6] = b[0].z; v[7] = b[0].w;
+#pragma unroll
+  for (int r = 1; r < S; ++r) {
+    v[0] += a[r].x; v[1] += a[r].y; v[2] += a[r].z; v[3] += a[r].w;
+    v[4] += b[r].x; v[5] += b[r].y; v[6] += b[r].z; v[7] += b[r].w;
+  }
+}
+
 template <typename Params>
 __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sf_smem = smem + kTRing;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sf_smem + kTSfSets * kTSfSetBytes);
-  uint64_t* empty = full + kTStages;
-  uint64_t* sf_full = empty + kTStages;
+  const uint32_t stages = (uint32_t)p.stages;
+  uint8_t* sf_smem = smem + stages * kTStageBytes;
+  float* slope = reinterpret_cast<float*>(sf_smem + kTSfSets * kTSfSet);
+  uint64_t* full = reinterpret_cast<uint64_t*>(slope + kF8SlopeTable);
+  uint64_t* empty = full + kTMaxStages;
+  uint64_t* sf_full = empty + kTMaxStages;
   uint64_t* sf_empty = sf_full + kTSfSets;
   uint64_t* done = sf_empty + kTSfSets;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* cta_max = reinterpret_cast<float*>(tmem_slot + 2);  // this CTA's block maximum
+  float* cta_max = reinterpret_cast<float*>(tmem_slot + 2);  // this CTA's maximum
   float* warp_max = cta_max + 1;                             // [8]
-  float* slope = reinterpret_cast<float*>(sf_smem + kTSfSets * kTSfSetBytes + 256);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -116,7 +145,7 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
 
   if (g.epi == kF8EpiRelu2Backward) f8_slope_init(slope, g.saved.e5m2, threadIdx.x, kTThreads);
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kTStages; ++s) {
+    for (uint32_t s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -159,17 +188,18 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
       bool ok = true;
       for (; issued < nkb; ++issued) {
         if (!bar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag)) { ok = false; break; }
-        expect_tx_at(full0 + 8 * stage, kTStageBytes);
         const uint32_t a_dst = ring + stage * kTStageBytes;
+        expect_tx_at(full0 + 8 * stage, kTStageBytes);
         tma_load_2d_local(a_dst, ma, &full[stage], ax, ay);
         tma_load_2d_local(a_dst + kTOperand, mb, &full[stage], bx, by);
         ax += adx; ay += ady; bx += bdx; by += bdy;
-        if (++stage == kTStages) { stage = 0; phase ^= 1u; }
+        if (++stage == stages) { stage = 0; phase ^= 1u; }
       }
-      if (!ok) give_up();
-      // every copy has landed before the ring's space is used again or the CTA exits
-      for (int i = max(0, issued - kTStages); i < issued; ++i)
-        (void)bar_wait(smem_u32(&full[i % kTStages]), (uint32_t)((i / kTStages) & 1), nullptr);
+      if (!ok || *abort_flag) {
+        give_up();
+        spin_ns(kAbortGraceNs);  // copies already issued land within microseconds
+      }
+      // (without an abort the issuing thread has seen every copy land before `done`)
     }
   } else if (warp == 1) {
     if (elect_one()) {
@@ -186,7 +216,7 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
         // need no barrier of their own
         const uint32_t sfa = tmem + kTSfCol + (set & 1u) * 8, sfb = sfa + 4;
         if (!bar_wait(sf_full0 + 8 * set, sf_phase, abort_flag)) { ok = false; break; }
-        const uint64_t src = sf_desc + (uint64_t)(set * (kTSfSetBytes >> 4));
+        const uint64_t src = sf_desc + (uint64_t)(set * (kTSfSet >> 4));
         f8_copy_sf(sfa, src);
         f8_copy_sf(sfb, src + (kF8SfBytes >> 4));
         const int n = min(kF8Group, nkb - kb);
@@ -195,19 +225,18 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
           if (!bar_wait(full0 + 8 * stage, phase, abort_flag)) { ok = false; break; }
           const uint64_t ad = ring_desc + (uint64_t)(stage * (kTStageBytes >> 4)), bd = ad + (kTOperand >> 4);
           const uint32_t id = f8_idesc_sf(idesc, q);
-          f8_mma(tmem, ad, bd, id, sfa, sfb, accumulate);
-          accumulate = 1;
 #pragma unroll
-          for (int k = 1; k < 4; ++k) f8_mma(tmem, ad + k * a_step, bd + k * b_step, id, sfa, sfb, 1u);
+          for (int k = 0; k < 4; ++k)
+            f8_mma(tmem, ad + k * a_step, bd + k * b_step, id, sfa, sfb, k ? 1u : accumulate);
+          accumulate = 1;
           f8_commit_at(empty0 + 8 * stage);
-          if (++stage == kTStages) { stage = 0; phase ^= 1u; }
+          if (++stage == stages) { stage = 0; phase ^= 1u; }
         }
         f8_commit_at(sf_empty0 + 8 * set);
         if (++set == kTSfSets) { set = 0; sf_phase ^= 1u; }
       }
       if (!ok) give_up();
-      f8_commit(done);
-      (void)bar_wait(smem_u32(done), 0, nullptr);  // every MMA and copy issued here is complete
+      f8_commit_at(smem_u32(done));  // arrives once everything issued here is complete
     }
   } else if (warp < 4) {
     // warps 2 and 3 take the groups of 512 codes in turn
@@ -224,7 +253,7 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
         if (lane == 0) give_up();
         break;
       }
-      uint8_t* dst = sf_smem + set * kTSfSetBytes + lane * 16;
+      uint8_t* dst = sf_smem + set * kTSfSet + lane * 16;
       *reinterpret_cast<uint4*>(dst) = wa;
       *reinterpret_cast<uint4*>(dst + kF8SfBytes) = wb;
       fence_async_smem();
@@ -234,20 +263,22 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
     }
   }
 
-  // the accumulator is final (the issuing thread waited for it) and the ring is free
+  // the accumulator is final and the ring free once `done` completes
+  if (lane == 0) (void)bar_wait(smem_u32(done), 0, nullptr);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  float* stage = reinterpret_cast<float*>(smem);
+  float* stage_f = reinterpret_cast<float*>(smem);
   {
-    const int quad = warp & 3, half = warp >> 2;
-    float* dst = stage + (32 * quad + lane) * kTPitch + 64 * half;
+    const int quad = warp & 3, side = warp >> 2;
+    constexpr int kChunks = 2;  // 32 columns each
+    float* dst = stage_f + (32 * quad + lane) * kTPitch + 32 * kChunks * side;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < kChunks; ++c) {
       float v[32];
       if (nkb > 0) {
-        tmem_ld32(tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(64 * half + 32 * c), v);
+        tmem_ld32(tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(32 * kChunks * side + 32 * c), v);
       } else {
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = 0.f;
@@ -270,30 +301,24 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
   const int rows_here = kT / split;
   const int iters = rows_here / 16;
   const int cl = (threadIdx.x & 15) * 8;
-  const int col = col_t + cl;
-  const uint32_t stage_addr = smem_u32(stage);
-  auto fetch = [&](int rl, float* v) {  // row rl of the tile: partial sums in rank order
-    const uint32_t off = (uint32_t)(rl * kTPitch + cl) * 4;
+  const uint32_t stage_addr = smem_u32(stage_f);
+  auto fetch = [&](int rl, float* v) {  // row rl of the tile
     if (split == 1) {
-      const float4 a = *reinterpret_cast<const float4*>(stage + rl * kTPitch + cl);
-      const float4 b = *reinterpret_cast<const float4*>(stage + rl * kTPitch + cl + 4);
+      const float4* q = reinterpret_cast<const float4*>(stage_f + rl * kTPitch + cl);
+      const float4 a = q[0], b = q[1];
       v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
       v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-      return;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.f;
-    for (int r = 0; r < split; ++r) {
-      const uint32_t at = peer_addr(stage_addr + off, (uint32_t)r);
-      const float4 a = ld_cluster_f4(at), b = ld_cluster_f4(at + 16);
-      v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-      v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    } else if (split == 2) {
+      fetch_split<2>(stage_addr + (uint32_t)(rl * kTPitch + cl) * 4, v);
+    } else {
+      fetch_split<4>(stage_addr + (uint32_t)(rl * kTPitch + cl) * 4, v);
     }
   };
 
-  // rows of this CTA end at row_end; entries past the matrix are kept at 0
+  // rows of this CTA end at row_end
   const int row0 = row_t + rank * rows_here + (threadIdx.x >> 4);
   const int row_end = min(g.m, row_t + (rank + 1) * rows_here);
+  const int col = col_t + cl;
   if (g.d8.codes == nullptr) {
     for (int i = 0; i < iters; ++i) {
       const int row = row0 + 16 * i;
@@ -303,23 +328,24 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
       if (g.d.vec) {
         if (row < row_end && col < g.n) f8_store8(g.d, row, col, g.n, v[0]);
       } else {  // through this CTA's own row of the staged tile, which no peer reads
-        f8_store_rows_xch<1>(g.d, row, 16, row_end, col, g.n, v, stage + (row - row_t) * kTPitch);
+        f8_store_rows_xch<1>(g.d, row, 16, row_end, col, g.n, v, stage_f + (row - row_t) * kTPitch);
       }
     }
   } else {
     // finished values go back to this CTA's own rows of the staged tile (no peer reads
-    // those), 4 rows per thread at a time, until the block's maximum is known
+    // those), a few rows per thread at a time, until the block's maximum is known
     auto put = [&](int rl, const float* v) {
-      *reinterpret_cast<float4*>(stage + rl * kTPitch + cl) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4*>(stage + rl * kTPitch + cl + 4) = make_float4(v[4], v[5], v[6], v[7]);
+      float4* q = reinterpret_cast<float4*>(stage_f + rl * kTPitch + cl);
+      q[0] = make_float4(v[0], v[1], v[2], v[3]);
+      q[1] = make_float4(v[4], v[5], v[6], v[7]);
     };
     auto get = [&](int rl, float* v) {
-      const float4 x = *reinterpret_cast<const float4*>(stage + rl * kTPitch + cl);
-      const float4 y = *reinterpret_cast<const float4*>(stage + rl * kTPitch + cl + 4);
+      const float4* q = reinterpret_cast<const float4*>(stage_f + rl * kTPitch + cl);
+      const float4 x = q[0], y = q[1];
       v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
       v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
     };
-    constexpr int kC = 4;
+    constexpr int kC = 2;
     float vmax = 0.f;
     for (int i0 = 0; i0 < iters; i0 += kC) {
       float v[kC][8], rmax[kC];
@@ -393,16 +419,17 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
     }
   }
   __syncwarp();
-  if (split > 1) cluster_sync_all();  // peers have read this CTA's partial tile and maximum
+  if (split > 1) cluster_sync_all();  // peers have read this CTA's partial tile and maxima
 }
 
 template <typename Params>
 cudaError_t launch_tile(const Params& p, int split, cudaStream_t st) {
   if (p.total_tiles == 0) return cudaSuccess;
   static std::atomic<uint64_t> ready{0};
-  const cudaError_t e = f8_allow_smem(reinterpret_cast<const void*>(fp8_tile_kernel<Params>), kTSmem, ready);
+  const cudaError_t e =
+      f8_allow_smem(reinterpret_cast<const void*>(fp8_tile_kernel<Params>), tile_smem(kTMaxStages), ready);
   if (e != cudaSuccess) return e;
-  return f8_launch(fp8_tile_kernel<Params>, p, p.total_tiles * split, kTThreads, kTSmem, split, st);
+  return f8_launch(fp8_tile_kernel<Params>, p, p.total_tiles * split, kTThreads, tile_smem(p.stages), split, st);
 }
 
 }  // namespace

@@ -1,7 +1,6 @@
 // Host side of the 8-bit operators: argument checks, kernel parameters and tensor maps,
 // launches.  Nothing is kept between calls but the handle's status word.
 #include <algorithm>
-#include <cstdlib>
 #include <vector>
 
 #include <nvtx3/nvToolsExt.h>
@@ -271,16 +270,6 @@ F8Scales scales_of(const muon_fp8_matrix& x, bool mn) {
   return s;
 }
 
-// CTAs that share one tile's contraction: doubled while the launch still fits the SMs
-// (two CTAs each) and every CTA keeps at least two k-blocks.
-int choose_split(int64_t tiles, int64_t kb, int sm_count) {
-  int split = 1;
-  static const int force = getenv("F8SPLIT") ? atoi(getenv("F8SPLIT")) : 0;
-  if (force) return force;
-  while (split < 8 && tiles * split * 2 <= 2 * sm_count && kb >= 4 * split) split *= 2;
-  return split;
-}
-
 struct ProductSize {
   int32_t m, n, k;
 };
@@ -353,15 +342,44 @@ muon_status launch_pair_products(muon_handle* h, const muon_fp8_product* product
   return MUON_OK;
 }
 
+// How a run of products is launched.
+struct Shape {
+  bool persistent = false;  // 256 x 256 tiles by pairs of CTAs that take tile after tile
+  int split = 1;            // otherwise a CTA per 128 x 128 tile: CTAs sharing its contraction
+  int stages = 6;           // and its ring
+};
+
+// tiles: 128 x 128 tiles of all products; min_kb: shortest contraction in blocks of 128.
+// Times in a chain of calls on one B200:
+//   up to one tile per SM: a CTA per tile (64 x 512 x 512: 5.3 us, persistent 6.6; 1536 x 1536 x
+//   4096: 12.6, 16.2), its contraction split while the SMs hold all parts and each keeps 8
+//   blocks or more (128 x 1536 x 6144: whole 14.4, in two 10.9, in four 10.0; 2048 x 512 x
+//   1024, parts of 4 blocks: whole 7.1, in two 8.0).
+//   up to two per SM with short contractions: two CTAs per SM with half the ring (1536 x 2048 x
+//   512: 7.6, persistent 8.3; at 2048 x 2048 x 4096: 19.4, 17.3).
+//   more: persistent pairs (4096 x 4096 x 1024: 19.7, a CTA per tile 35).
+Shape choose_shape(int64_t tiles, int64_t min_kb, int sm_count) {
+  Shape sh;
+  if (tiles <= sm_count) {
+    while (sh.split < 4 && tiles * sh.split * 2 <= sm_count && min_kb >= 16 * sh.split) sh.split *= 2;
+    return sh;
+  }
+  sh.stages = 3;
+  sh.persistent = min_kb > 0 && (tiles > 2 * sm_count || min_kb >= 16);
+  return sh;
+}
+
 template <int N>
 muon_status launch_tile_products(muon_handle* h, const muon_fp8_product* products, const int* live, int count,
-                                 cudaStream_t st) {
+                                 const Shape& sh, cudaStream_t st) {
   F8GemmParamsN<N> p;
   int64_t tiles = 0, min_kb = 0;
-  const muon_status s = fill_products(h, p, products, live, count, kFp8Block, &tiles, &min_kb);
+  const muon_status s =
+      fill_products(h, p, products, live, count, kFp8Block, &tiles, &min_kb);
   if (s) return s;
+  p.stages = sh.stages;
   prof_begin(h, st, kFp8KindBase + MUON_FP8_KIND_MATMUL);
-  const cudaError_t e = launch_fp8_gemm_tile(p, choose_split(tiles, min_kb, h->sm_count), st);
+  const cudaError_t e = launch_fp8_gemm_tile(p, sh.split, st);
   prof_end(h, kFp8KindBase + MUON_FP8_KIND_MATMUL, st);
   if (e != cudaSuccess) return cuda_fail(h, e, "8-bit product launch");
   h->last_launches++;
@@ -371,24 +389,25 @@ muon_status launch_tile_products(muon_handle* h, const muon_fp8_product* product
 // The products products[live[..]], in launches of a few.
 muon_status launch_products(muon_handle* h, const muon_fp8_product* products, const std::vector<int>& live,
                             cudaStream_t st) {
-  static const int thr = getenv("F8PAIR") ? atoi(getenv("F8PAIR")) : 37;
   for (size_t b = 0; b < live.size();) {
-    // a run of products of one kind of kernel
-    int64_t pair_tiles = 0;
-    bool pair = true;
-    const int few = (int)std::min<size_t>(kF8PairProducts, live.size() - b);
-    for (int i = 0; i < few; ++i) {
-      const ProductSize sz = size_of(products[live[b + i]]);
-      pair_tiles += ((int64_t)sz.m + kF8PairTile - 1) / kF8PairTile * ((sz.n + kF8PairTile - 1) / kF8PairTile);
-      pair = pair && sz.k > 0;
-    }
-    pair = pair && pair_tiles >= thr;
-    const int count = pair ? few : (int)std::min<size_t>(kMaxF8Products, live.size() - b);
+    int count = (int)std::min<size_t>(kMaxF8Products, live.size() - b);
     const int* items = live.data() + b;
-    const muon_status s =
-        pair ? launch_pair_products(h, products, items, count, st)
-             : count <= kF8FewProducts ? launch_tile_products<kF8FewProducts>(h, products, items, count, st)
-                                       : launch_tile_products<kMaxF8Products>(h, products, items, count, st);
+    Shape sh;
+    while (true) {
+      int64_t tiles = 0, min_kb = INT64_MAX;
+      for (int i = 0; i < count; ++i) {
+        const ProductSize z = size_of(products[items[i]]);
+        tiles += blocks_of(z.m) * blocks_of(z.n);
+        min_kb = std::min(min_kb, blocks_of(z.k));
+      }
+      sh = choose_shape(tiles, min_kb, h->sm_count);
+      if (!sh.persistent || count <= kF8PairProducts) break;
+      count = kF8PairProducts;
+    }
+    const muon_status s = sh.persistent ? launch_pair_products(h, products, items, count, st)
+                          : count <= kF8FewProducts
+                              ? launch_tile_products<kF8FewProducts>(h, products, items, count, sh, st)
+                              : launch_tile_products<kMaxF8Products>(h, products, items, count, sh, st);
     if (s) return s;
     b += (size_t)count;
   }

@@ -72,8 +72,9 @@ def test_exact_formats_and_row_blocks(h, fa, fb, ba, bb):
 
 
 def test_exact_many_tiles_and_long_contractions(h):
-    """Grids of more tiles than the GPU holds at once, and few tiles with a long K."""
-    for M, N, K in [(2600, 2700, 300), (4096, 2304, 768), (256, 256, 8192), (512, 384, 8100), (8192, 130, 128)]:
+    """Persistent pairs of CTAs, two tiles per SM, and few tiles with a long K (split)."""
+    for M, N, K in [(2600, 2700, 300), (4096, 2304, 768), (256, 256, 8192), (512, 384, 8100), (8192, 130, 128),
+                    (1536, 2048, 300), (1, 40000, 129), (40000, 1, 129), (130, 1400, 2100), (2100, 2048, 2048)]:
         for ta, tb in [(False, True), (True, False)]:
             a, b, va, vb = operands(M, N, K, ta, tb, seed=K)
             d = torch.empty(M, N, device="cuda")
@@ -167,6 +168,109 @@ def test_eight_bit_results_are_exact(h, blocks, M, N, K):
     d = torch.empty(M, N, device="cuda")
     mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, d, trans_b=True, epilogue="relu2_backward", saved=saved)])
     np.testing.assert_array_equal(d.double().cpu().numpy(), ref)
+
+
+def quantized_equal(out, ref):
+    c, e = fp8.quantize(ref, out.format, out.blocks)
+    np.testing.assert_array_equal(exps(out), e)
+    np.testing.assert_array_equal(values(out), fp8.dequantize(c, e, out.format, out.blocks))
+
+
+BIG = (2350, 2195, 260)        # 342 tiles of 128 x 128: persistent pairs; nothing a multiple of 16
+
+
+def roots(M, N, fmt, blocks, seed):
+    """A checkpoint of 0, 1, 4, 16 under scales 2^-2, 1, 2^2: exact square roots."""
+    saved = mb.Fp8Matrix(M, N, format=fmt, blocks=blocks)
+    rng = np.random.default_rng(seed)
+    vals = fp8.code_values(fmt)
+    table = np.array([int(np.flatnonzero(vals == v)[0]) for v in (0, 1, 4, 16)], dtype=np.uint8)
+    saved.codes[:, :N] = torch.from_numpy(table[rng.integers(0, 4, (M, N))]).cuda()
+    saved.scales.copy_(torch.from_numpy((127 + 2 * rng.integers(-1, 2, tuple(saved.scales.shape))).astype(np.uint8)))
+    return saved
+
+
+@pytest.mark.parametrize("epi", ["none", "relu2", "relu2_backward"])
+@pytest.mark.parametrize("add", [False, True])
+@pytest.mark.parametrize("saved_fmt,saved_blocks", [("e4m3", "square"), ("e5m2", "row")])
+def test_every_kind_of_result_of_many_tiles(h, epi, add, saved_fmt, saved_blocks):
+    if epi != "relu2_backward" and saved_fmt == "e5m2":
+        pytest.skip("no checkpoint in this epilogue")
+    M, N, K = BIG
+    a, b, va, vb = operands(M, N, K, False, True, seed=3)
+    c = torch.randint(-9, 10, (M, N), device="cuda").float() if add else None
+    base = va @ vb + (c.double().cpu().numpy() if add else 0.0)
+    saved = roots(M, N, saved_fmt, saved_blocks, 5) if epi == "relu2_backward" else None
+    ref = {"none": base, "relu2": fp8.relu2(base),
+           "relu2_backward": fp8.relu2_backward(base, values(saved)) if saved else None}[epi]
+    ref = ref.astype(np.float32).astype(np.float64)
+    kw = dict(trans_b=True, epilogue=epi, saved=saved)
+    for dt in ("bf16", "fp32"):
+        for pitch, off in ((N, 0), (N + 13, 5), (N + 5, 0)):          # rows of every alignment
+            big = torch.full((M, pitch), 3.0, dtype=DT[dt], device="cuda")
+            d = big[:, off:off + N]
+            cc = None
+            if add:
+                cc = c.to(DT[dt])
+            mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, d, add=cc, **kw)])
+            want = torch.from_numpy(ref).to(DT[dt])
+            assert torch.equal(d.cpu(), want), (dt, pitch)
+            rest = torch.cat([big[:, :off], big[:, off + N:]], dim=1)
+            assert (rest == 3).all()
+    for blocks in ("square", "row"):
+        out = mb.Fp8Matrix(M, N, blocks=blocks)
+        out.codes.fill_(0xEE)
+        mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, out, add=c, **kw)])
+        quantized_equal(out, ref)
+        assert (out.codes[:, N:] == 0xEE).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 520, 256), (200, 140, 4096), BIG])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("blocks", ["square", "row"])
+def test_non_finite_sums_in_eight_bits(h, M, N, K, fmt, blocks):
+    """Infinities and NaN do not reach the scale; they become the format's own."""
+    a, b, va, vb = operands(M, N, K, False, True, seed=8)
+    c = torch.zeros(M, N, device="cuda")
+    c[0, 0], c[M - 1, N - 1], c[130, 131], c[150, :128] = float("inf"), float("nan"), -float("inf"), float("inf")
+    ref = va @ vb + c.double().cpu().numpy()
+    out = mb.Fp8Matrix(M, N, format=fmt, blocks=blocks)
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, out, trans_b=True, add=c)])
+    quantized_equal(out, ref)
+    # an 8-bit operand with a NaN entry: its row only
+    a.codes[5, 7] = 0x7f
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, out, trans_b=True)])
+    ref = va @ vb
+    ref[5, :] = np.nan
+    quantized_equal(out, ref)
+
+
+def test_launches_of_mixed_kinds(h):
+    """Results of different kinds in one persistent launch, more than one launch takes."""
+    M, N, K = 1300, 1100, 200
+    prods, checks = [], []
+    for i in range(10):
+        ta, tb = bool(i & 1), bool(i & 2)
+        a, b, va, vb = operands(M, N, K + i, ta, tb, seed=i)
+        want = va @ vb
+        kw = dict(trans_a=ta, trans_b=tb)
+        if i % 3 == 0:
+            out = torch.empty(M, N, device="cuda")
+        elif i % 3 == 1:
+            out = mb.Fp8Matrix(M, N, format="e5m2")
+        else:
+            out = torch.empty(M, N, device="cuda", dtype=torch.bfloat16)
+            kw["epilogue"], kw["saved"] = "relu2_backward", roots(M, N, "e4m3", "square", i)
+            want = fp8.relu2_backward(want, values(kw["saved"]))
+        prods.append(mb.Fp8Product(a, b, out, **kw))
+        checks.append((out, want))
+    mb.muon_fp8_matmul(h, prods)
+    mb.muon_sync(h)
+    for out, want in checks:
+        if isinstance(out, mb.Fp8Matrix):
+            quantized_equal(out, want)
+        else:
+            assert torch.equal(out.cpu(), torch.from_numpy(want).to(out.dtype))
 
 
 def test_list_of_products_mixed(h):
