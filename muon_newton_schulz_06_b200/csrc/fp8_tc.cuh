@@ -170,29 +170,73 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 
-// Scale words of row r0 + lane + 32 j (j = 0..3) for k-blocks kb0 .. kb0 + 3; rows and
-// k-blocks out of range take 2^0 (their codes are zero).
-__device__ __forceinline__ uint4 f8_sf_words(const F8Scales& s, int r0, int rows, int kb0, int nkb, int lane) {
+// Scale words of 128 rows from r0 on, for k-blocks kb0 .. kb0 + 3, four rows per lane; rows and
+// k-blocks out of range take 2^0 (their codes are zero).  f8_sf_load issues the loads,
+// f8_sf_store puts the words where the copy to tensor memory expects them (512 bytes at dst).
+// Lane l has rows l + 32 j, or, where all 128 rows exist (`quads`), rows 4 l + j: their four
+// bytes lie together, in one aligned word or two, in the place of four loads.
+struct F8SfWords {
   uint32_t w[4];
+  bool quads;
+};
+__device__ __forceinline__ F8SfWords f8_sf_load(const F8Scales& s, int r0, int rows, int kb0, int nkb, int lane) {
+  F8SfWords f;
+  f.quads = false;
   if (!s.by_row) {
     const uint8_t* p = s.s + (int64_t)(r0 / kFp8Block) * s.s_r + (int64_t)kb0 * s.s_k;
     uint32_t word = 0;
 #pragma unroll
     for (int q = 0; q < kF8Group; ++q)
       word |= (uint32_t)((r0 < rows && kb0 + q < nkb) ? p[(int64_t)q * s.s_k] : 127) << (8 * q);
-    w[0] = w[1] = w[2] = w[3] = word;
-  } else {
+    f.w[0] = f.w[1] = f.w[2] = f.w[3] = word;
+    return f;
+  }
+  const uint8_t* p = s.s + r0 + (int64_t)kb0 * s.s_k;  // s_r is 1
+  f.quads = r0 + kFp8Block <= rows;
+  if (f.quads) {
+    uint32_t x[4];
+#pragma unroll
+    for (int q = 0; q < kF8Group; ++q) {
+      const uint8_t* at = p + (int64_t)q * s.s_k + 4 * lane;
+      const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(at) & 3u);  // the same in all lanes
+      const uint32_t* word = reinterpret_cast<const uint32_t*>(at - off);
+      x[q] = 0x7f7f7f7fu;
+      if (kb0 + q < nkb) x[q] = off == 0 ? word[0] : __funnelshift_r(word[0], word[1], 8 * off);
+    }
+    // byte j of the four loads makes row j's word
+    const uint32_t a = __byte_perm(x[0], x[1], 0x5140), b = __byte_perm(x[2], x[3], 0x5140);
+    const uint32_t c = __byte_perm(x[0], x[1], 0x7362), d = __byte_perm(x[2], x[3], 0x7362);
+    f.w[0] = __byte_perm(a, b, 0x5410);
+    f.w[1] = __byte_perm(a, b, 0x7632);
+    f.w[2] = __byte_perm(c, d, 0x5410);
+    f.w[3] = __byte_perm(c, d, 0x7632);
+    return f;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = lane + 32 * j;
+    f.w[j] = 0;
+#pragma unroll
+    for (int q = 0; q < kF8Group; ++q)
+      f.w[j] |= (uint32_t)((r0 + r < rows && kb0 + q < nkb) ? p[(int64_t)q * s.s_k + r] : 127) << (8 * q);
+  }
+  return f;
+}
+__device__ __forceinline__ void f8_sf_store(uint8_t* dst, const F8SfWords& f, int lane) {
+  if (f.quads) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int r = r0 + lane + 32 * j;
-      const uint8_t* p = s.s + (int64_t)r * s.s_r + (int64_t)kb0 * s.s_k;
-      w[j] = 0;
-#pragma unroll
-      for (int q = 0; q < kF8Group; ++q)
-        w[j] |= (uint32_t)((r < rows && kb0 + q < nkb) ? p[(int64_t)q * s.s_k] : 127) << (8 * q);
+      const int r = 4 * lane + j;
+      *reinterpret_cast<uint32_t*>(dst + (r & 31) * 16 + (r >> 5) * 4) = f.w[j];
     }
+  } else {
+    *reinterpret_cast<uint4*>(dst + lane * 16) = make_uint4(f.w[0], f.w[1], f.w[2], f.w[3]);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Brings a tensor map (a kernel parameter) into the cache ahead of its first copy.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
 }  // namespace

@@ -14,7 +14,7 @@
 // been brought from 15 to about 5.
 //
 // General (any pitch, alignment and width): 512 threads, a thread holds 8 consecutive columns of
-// rows t/16 + 32 i.
+// rows t/16 + 32 i; half a block with 256 threads where no maximum spans the block.
 //
 // In both, a group of lanes covers the 128 columns of a row: row scales need shuffles only,
 // square ones one exchange through shared memory.
@@ -23,12 +23,10 @@
 namespace muon {
 namespace {
 
-constexpr int kThreads = 512;
 constexpr int kIter = 4;
-constexpr int kStep = kThreads / 16;  // rows between a thread's rows
-static_assert(kIter * kStep == kFp8Block, "a CTA holds one block");
 
 // Maximum of m over the CTA.
+template <int kThreads>
 __device__ __forceinline__ float cta_max(float m, float* warp_max) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -39,12 +37,15 @@ __device__ __forceinline__ float cta_max(float m, float* warp_max) {
   return m;
 }
 
-template <int OP, typename Params>
-__global__ void __launch_bounds__(kThreads, 2) fp8_pass_kernel(const __grid_constant__ Params p) {
+// SUB: CTAs per block, 1 or 2.
+template <int OP, int SUB, typename Params>
+__global__ void __launch_bounds__(512 / SUB, 2 * SUB) fp8_pass_kernel(const __grid_constant__ Params p) {
+  constexpr int kThreads = 512 / SUB;
+  constexpr int kStep = kThreads / 16;  // rows between a thread's rows
   __shared__ float warp_max[2][kThreads / 32];
   __shared__ __align__(16) float xch_all[kThreads / 16 * kF8Xch];
   __shared__ float slope[OP == kF8ActBackward ? kF8SlopeTable : 1];
-  const int block = blockIdx.x;
+  const int block = blockIdx.x / SUB;
   int lo = 0, hi = p.n - 1;  // last matrix whose block_begin <= block
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -56,7 +57,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_pass_kernel(const __grid_cons
   const int br = local / m.blocks_c, bc = local - br * m.blocks_c;
   const int rows = m.rows, cols = m.cols;
   const int col = bc * kFp8Block + (threadIdx.x & 15) * 8;
-  const int row0 = br * kFp8Block + (threadIdx.x >> 4);
+  const int row0 = br * kFp8Block + (int)(blockIdx.x % SUB) * (kFp8Block / SUB) + (threadIdx.x >> 4);
 
   float* xch = xch_all + (threadIdx.x >> 4) * kF8Xch;
   if constexpr (OP == kF8ActBackward) {
@@ -115,11 +116,11 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_pass_kernel(const __grid_cons
     }
     float rmax[kIter], inv[kIter];
     f8_row_max<kIter>(v, rmax);
-    float amax = cta_max(fmaxf(fmaxf(rmax[0], rmax[1]), fmaxf(rmax[2], rmax[3])), warp_max[0]);
+    float amax = cta_max<kThreads>(fmaxf(fmaxf(rmax[0], rmax[1]), fmaxf(rmax[2], rmax[3])), warp_max[0]);
     const bool inf = amax == kF8Inf;
     if (inf) {
       f8_row_max_finite<kIter>(v, rmax);
-      amax = cta_max(fmaxf(fmaxf(rmax[0], rmax[1]), fmaxf(rmax[2], rmax[3])), warp_max[1]);
+      amax = cta_max<kThreads>(fmaxf(fmaxf(rmax[0], rmax[1]), fmaxf(rmax[2], rmax[3])), warp_max[1]);
     }
     const int e = f8_exponent(amax, m.out8.e5m2);
     if (threadIdx.x == 0) *f8_scale_at(m.out8, br * kFp8Block, bc) = (uint8_t)(e + 127);
@@ -129,13 +130,21 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_pass_kernel(const __grid_cons
   }
 }
 
+template <int OP, typename Params>
+cudaError_t launch_op(const Params& p, bool halves, cudaStream_t st) {
+  if (halves) return f8_launch<Params>(fp8_pass_kernel<OP, 2, Params>, p, 2 * p.total_blocks, 256, 0, 1, st);
+  return f8_launch<Params>(fp8_pass_kernel<OP, 1, Params>, p, p.total_blocks, 512, 0, 1, st);
+}
+
 template <typename Params>
 cudaError_t launch(int op, const Params& p, cudaStream_t st) {
   if (p.total_blocks == 0) return cudaSuccess;
+  bool halves = p.total_blocks <= INT32_MAX / 2;
+  for (int i = 0; i < p.n; ++i) halves = halves && (p.m[i].out8.codes == nullptr || p.m[i].out8.row_blocks);
   switch (op) {
-    case kF8Quantize: return f8_launch(fp8_pass_kernel<kF8Quantize, Params>, p, p.total_blocks, kThreads, 0, 1, st);
-    case kF8Dequantize: return f8_launch(fp8_pass_kernel<kF8Dequantize, Params>, p, p.total_blocks, kThreads, 0, 1, st);
-    default: return f8_launch(fp8_pass_kernel<kF8ActBackward, Params>, p, p.total_blocks, kThreads, 0, 1, st);
+    case kF8Quantize: return launch_op<kF8Quantize>(p, halves, st);
+    case kF8Dequantize: return f8_launch<Params>(fp8_pass_kernel<kF8Dequantize, 2, Params>, p, 2 * p.total_blocks, 256, 0, 1, st);
+    default: return launch_op<kF8ActBackward>(p, halves, st);
   }
 }
 
@@ -187,17 +196,20 @@ __device__ __forceinline__ uint4 encode16(const float* v, float inv, bool inf) {
   return make_uint4(a.x, a.y, b.x, b.y);
 }
 
-// OP; BF16: type of the dense side; FMT: format of the 8-bit result (of the source for
+constexpr int kF8ActBackward8 = 3;
+
+// OP (kF8ActBackward8: the gradient in 8 bits); BF16: type of the dense side; FMT: format of the 8-bit result (of the source for
 // dequantise), 1 = e5m2.  bf16: 256 threads, 4 rows each; float32: 512 threads, 2 rows.
 template <int OP, bool BF16, bool FMT>
-__global__ void __launch_bounds__(BF16 ? 256 : 512, BF16 ? (OP == kF8ActBackward ? 2 : 4) : 2)
+__global__ void __launch_bounds__(BF16 ? 256 : 512, BF16 ? (OP == kF8ActBackward8 ? 2 : OP == kF8ActBackward ? 3 : 4) : 2)
     fp8_wide_kernel(const __grid_constant__ F8PassParamsN<kF8FewPasses> p) {
   constexpr int kThr = BF16 ? 256 : 512;
   constexpr int kRows = kThr / 8;           // rows between a thread's rows
   constexpr int kN = kFp8Block / kRows;     // rows per thread
   constexpr int kW = BF16 ? 8 : 16;         // words per 16 entries
   __shared__ float warp_max[2][kThr / 32];
-  __shared__ float slope[OP == kF8ActBackward ? kF8SlopeTable : 1];
+  constexpr bool kGrad = OP == kF8ActBackward || OP == kF8ActBackward8;
+  __shared__ float slope[kGrad ? kF8SlopeTable : 1];
   int mi = 0;
   while (mi + 1 < p.n && p.m[mi + 1].block_begin <= (int)blockIdx.x) ++mi;
   const F8Pass& m = p.m[mi];
@@ -207,7 +219,7 @@ __global__ void __launch_bounds__(BF16 ? 256 : 512, BF16 ? (OP == kF8ActBackward
   const int col = bc * kFp8Block + (threadIdx.x & 7) * 16;
   const int row0 = br * kFp8Block + (threadIdx.x >> 3);
   const bool live_c = col < cols;
-  if constexpr (OP == kF8ActBackward) {
+  if constexpr (kGrad) {
     if (p.relu2) {
       f8_slope_init(slope, m.saved.e5m2, threadIdx.x, kThr);
       __syncthreads();
@@ -266,7 +278,7 @@ __global__ void __launch_bounds__(BF16 ? 256 : 512, BF16 ? (OP == kF8ActBackward
         for (int j = 0; j < 16; ++j) v[j] = f8_relu2(v[j]);
       }
     }
-    if constexpr (OP == kF8ActBackward) {
+    if constexpr (kGrad) {
       if (relu2) {
         const int e = (int)sb[i] - 127, parity = e & 1;
         const float scale = sb[i] == 255u ? __uint_as_float(0x7fc00000u) : f8_exp2((e - parity) / 2);
@@ -278,22 +290,19 @@ __global__ void __launch_bounds__(BF16 ? 256 : 512, BF16 ? (OP == kF8ActBackward
     }
   };
   if constexpr (OP == kF8ActBackward) {
-    if (m.out.data != nullptr) {
-      uint8_t* q = reinterpret_cast<uint8_t*>(m.out.data) + ((int64_t)row0 * m.out.ld + col) * (BF16 ? 2 : 4);
+    uint8_t* q = reinterpret_cast<uint8_t*>(m.out.data) + ((int64_t)row0 * m.out.ld + col) * (BF16 ? 2 : 4);
 #pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        float v[16];
-        values(i, v);
-        if (live_c && row0 + i * kRows < rows) store16<BF16>(q + (int64_t)(i * kRows) * m.out.ld * (BF16 ? 2 : 4), v);
-      }
-      return;
+    for (int i = 0; i < kN; ++i) {
+      float v[16];
+      values(i, v);
+      if (live_c && row0 + i * kRows < rows) store16<BF16>(q + (int64_t)(i * kRows) * m.out.ld * (BF16 ? 2 : 4), v);
     }
   }
-  if constexpr (OP != kF8Dequantize) {
+  if constexpr (OP == kF8Quantize || OP == kF8ActBackward8) {
     // the gradient's entries are formed once; those to quantise stay packed, and are unpacked
     // again for the codes
-    float g[OP == kF8ActBackward ? kN : 1][16];
-    if constexpr (OP == kF8ActBackward) {
+    float g[OP == kF8ActBackward8 ? kN : 1][16];
+    if constexpr (OP == kF8ActBackward8) {
 #pragma unroll
       for (int i = 0; i < kN; ++i) values(i, g[i]);
     }
@@ -301,7 +310,7 @@ __global__ void __launch_bounds__(BF16 ? 256 : 512, BF16 ? (OP == kF8ActBackward
     // monotonic, so relu^2 takes that of the largest entry
     auto row_max = [&](int i, bool finite) {
       float a = 0.f;
-      if constexpr (OP == kF8ActBackward) {
+      if constexpr (OP == kF8ActBackward8) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) a = fmaxf(a, finite ? f8_finite_abs(g[i][j]) : fabsf(g[i][j]));
       } else if (finite) {
@@ -375,7 +384,7 @@ __global__ void __launch_bounds__(BF16 ? 256 : 512, BF16 ? (OP == kF8ActBackward
       if (row < rows && (m.out8.row_blocks ? (threadIdx.x & 7) == 0 : threadIdx.x == 0 && i == 0))
         *f8_scale_at(m.out8, row, bc) = (uint8_t)(e + 127);
       uint4 code;
-      if constexpr (OP == kF8ActBackward) {
+      if constexpr (OP == kF8ActBackward8) {
         code = encode16<FMT>(g[i], f8_exp2(-e), inf);
       } else {
         float v[16];
@@ -398,7 +407,8 @@ bool wide(int op, const F8PassParamsN<kF8FewPasses>& p, bool* bf16, bool* e5m2) 
     if (m.cols % 16) return false;
     const F8Dense& x = op == kF8Dequantize ? m.out : m.in;
     if (!wide_dense(x)) return false;
-    if (op == kF8ActBackward && m.out.data != nullptr && (!wide_dense(m.out) || m.out.bf16 != m.in.bf16)) return false;
+    if (op == kF8ActBackward && (m.out.data == nullptr || !wide_dense(m.out) || m.out.bf16 != m.in.bf16)) return false;
+    if (op == kF8ActBackward8 && m.out8.codes == nullptr) return false;
     const bool f = op == kF8Dequantize ? m.saved.e5m2 : m.out8.codes != nullptr && m.out8.e5m2;
     if (i == 0) {
       *bf16 = x.bf16;
@@ -410,25 +420,29 @@ bool wide(int op, const F8PassParamsN<kF8FewPasses>& p, bool* bf16, bool* e5m2) 
   return true;
 }
 
-template <int OP>
-cudaError_t launch_wide(const F8PassParamsN<kF8FewPasses>& p, bool bf16, bool e5m2, cudaStream_t st) {
+template <int OP, bool FMT>
+cudaError_t launch_wide(const F8PassParamsN<kF8FewPasses>& p, bool bf16, cudaStream_t st) {
   using P = F8PassParamsN<kF8FewPasses>;
-  if (bf16)
-    return e5m2 ? f8_launch<P>(fp8_wide_kernel<OP, true, true>, p, p.total_blocks, 256, 0, 1, st)
-                : f8_launch<P>(fp8_wide_kernel<OP, true, false>, p, p.total_blocks, 256, 0, 1, st);
-  return e5m2 ? f8_launch<P>(fp8_wide_kernel<OP, false, true>, p, p.total_blocks, 512, 0, 1, st)
-              : f8_launch<P>(fp8_wide_kernel<OP, false, false>, p, p.total_blocks, 512, 0, 1, st);
+  return bf16 ? f8_launch<P>(fp8_wide_kernel<OP, true, FMT>, p, p.total_blocks, 256, 0, 1, st)
+              : f8_launch<P>(fp8_wide_kernel<OP, false, FMT>, p, p.total_blocks, 512, 0, 1, st);
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_pass(int op, const F8PassParamsN<kF8FewPasses>& p, cudaStream_t st) {
   bool bf16 = false, e5m2 = false;
-  if (p.total_blocks > 0 && wide(op, p, &bf16, &e5m2)) {
-    switch (op) {
-      case kF8Quantize: return launch_wide<kF8Quantize>(p, bf16, e5m2, st);
-      case kF8Dequantize: return launch_wide<kF8Dequantize>(p, bf16, e5m2, st);
-      default: return launch_wide<kF8ActBackward>(p, bf16, e5m2, st);
+  const int wide_op = op == kF8ActBackward && p.m[0].out8.codes != nullptr ? (int)kF8ActBackward8 : op;
+  if (p.total_blocks > 0 && wide(wide_op, p, &bf16, &e5m2)) {
+    switch (wide_op) {
+      case kF8Quantize:
+        return e5m2 ? launch_wide<kF8Quantize, true>(p, bf16, st) : launch_wide<kF8Quantize, false>(p, bf16, st);
+      case kF8Dequantize:
+        return e5m2 ? launch_wide<kF8Dequantize, true>(p, bf16, st) : launch_wide<kF8Dequantize, false>(p, bf16, st);
+      case kF8ActBackward:  // no 8-bit result
+        return launch_wide<kF8ActBackward, false>(p, bf16, st);
+      default:
+        return e5m2 ? launch_wide<kF8ActBackward8, true>(p, bf16, st)
+                    : launch_wide<kF8ActBackward8, false>(p, bf16, st);
     }
   }
   return launch(op, p, st);

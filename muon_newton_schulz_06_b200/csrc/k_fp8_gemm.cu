@@ -157,6 +157,10 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (threadIdx.x == 0 && nkb > 0) {
+    prefetch_map(&p.map_a[gi]);
+    prefetch_map(&p.map_b[gi]);
+  }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(kTTmemCols)
@@ -244,8 +248,8 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
     uint32_t set = warp - 2, phase = 1;
     for (int i = warp - 2; i < groups; i += 2) {
       const int kb = kb_begin + i * kF8Group;
-      const uint4 wa = f8_sf_words(g.sa, row_t, g.m, kb, nkb_all, lane);
-      const uint4 wb = f8_sf_words(g.sb, col_t, g.n, kb, nkb_all, lane);
+      const F8SfWords wa = f8_sf_load(g.sa, row_t, g.m, kb, nkb_all, lane);
+      const F8SfWords wb = f8_sf_load(g.sb, col_t, g.n, kb, nkb_all, lane);
       int ok = 1;
       if (lane == 0) ok = bar_wait(smem_u32(&sf_empty[set]), phase, abort_flag);
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -253,9 +257,9 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
         if (lane == 0) give_up();
         break;
       }
-      uint8_t* dst = sf_smem + set * kTSfSet + lane * 16;
-      *reinterpret_cast<uint4*>(dst) = wa;
-      *reinterpret_cast<uint4*>(dst + kF8SfBytes) = wb;
+      uint8_t* dst = sf_smem + set * kTSfSet;
+      f8_sf_store(dst, wa, lane);
+      f8_sf_store(dst + kF8SfBytes, wb, lane);
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sf_full[set]);

@@ -224,6 +224,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == 0 && lane < p.n) {
+    prefetch_map(&p.map_a[lane]);
+    prefetch_map(&p.map_b[lane]);
+  }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(512)
@@ -350,9 +354,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       const F8Product& g = p.p[tl.gi];
       for (int kb = 0; kb < tl.nkb; kb += kF8Group) {
         if ((turn++ & 1u) != mine) continue;
-        const uint4 wa = f8_sf_words(g.sa, tl.row + (int)rank * 128, g.m, kb, tl.nkb, lane);
-        const uint4 w0 = f8_sf_words(g.sb, tl.col, g.n, kb, tl.nkb, lane);
-        const uint4 w1 = f8_sf_words(g.sb, tl.col + 128, g.n, kb, tl.nkb, lane);
+        const F8SfWords wa = f8_sf_load(g.sa, tl.row + (int)rank * 128, g.m, kb, tl.nkb, lane);
+        const F8SfWords w0 = f8_sf_load(g.sb, tl.col, g.n, kb, tl.nkb, lane);
+        const F8SfWords w1 = f8_sf_load(g.sb, tl.col + 128, g.n, kb, tl.nkb, lane);
         int got = 1;
         if (lane == 0) got = bar_wait(smem_u32(&sf_empty[set]), phase, abort_flag);
         got = __shfl_sync(0xffffffffu, got, 0);
@@ -361,10 +365,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
           ok = false;
           break;
         }
-        uint8_t* dst = sf_smem + set * kPSfSet + lane * 16;
-        *reinterpret_cast<uint4*>(dst) = wa;
-        *reinterpret_cast<uint4*>(dst + kF8SfBytes) = w0;
-        *reinterpret_cast<uint4*>(dst + 2 * kF8SfBytes) = w1;
+        uint8_t* dst = sf_smem + set * kPSfSet;
+        f8_sf_store(dst, wa, lane);
+        f8_sf_store(dst + kF8SfBytes, w0, lane);
+        f8_sf_store(dst + 2 * kF8SfBytes, w1, lane);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) remote_arrive(leader_full0 + 8 * set);
