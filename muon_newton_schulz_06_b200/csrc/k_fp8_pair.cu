@@ -29,6 +29,8 @@
 // 132 us per 8192 x 6144 x 1536 product with loads one chunk ahead and the shared columns in
 // registers).
 // Every wait is bounded, the exchange of the maxima included.
+#include <type_traits>
+
 #include "fp8_blocks.cuh"
 #include "fp8_tc.cuh"
 
@@ -132,7 +134,8 @@ __device__ __noinline__ uint2 encode_inf8(float4 a, float4 b, uint2 c, bool e5m2
 }
 
 // 32 consecutive entries of this thread's row of the addend (row0 + lane, col ..).
-template <bool BF16>
+// VEC: whole 32 columns in rows that 16-byte loads can address.
+template <bool BF16, bool VEC>
 __device__ __forceinline__ void add_c32(const F8Dense& c, uint8_t* blk, int row0, int rows, int col, int cols,
                                         float (&v)[32]) {
   constexpr int kEsz = BF16 ? 2 : 4;
@@ -145,7 +148,7 @@ __device__ __forceinline__ void add_c32(const F8Dense& c, uint8_t* blk, int row0
     const int valid = min(32, (cols - col) * kEsz - 32 * i);
     if (valid <= 0) break;
     uint4 x[2];
-    if (c.vec && valid == 32) {
+    if (VEC || (c.vec && valid == 32)) {
       const uint4* q = reinterpret_cast<const uint4*>(src + lane * pitch + 32 * i);
       x[0] = live ? q[0] : make_uint4(0u, 0u, 0u, 0u);
       x[1] = live ? q[1] : make_uint4(0u, 0u, 0u, 0u);
@@ -456,11 +459,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       if (shared_c >= 0 && shared_c >= chunks) release_shared();
 
       // addend, activation or its gradient
-      auto finish = [&](int c, float (&v)[32]) {
+      // PLAIN: no chunk needs the calls for unaligned rows and edges.  The loops that most
+      // tiles take hold no call at all: with the rare paths inside them an 8-bit tile's second
+      // reading took 4,500 clocks.
+      auto finish = [&](auto plain, int c, float (&v)[32]) {
+        constexpr bool PLAIN = decltype(plain)::value;
         const int col = col0 + 32 * c;
         if (add) {
-          if (g.c.bf16) add_c32<true>(g.c, blk, row0, g.m, col, g.n, v);
-          else add_c32<false>(g.c, blk, row0, g.m, col, g.n, v);
+          if (g.c.bf16) add_c32<true, PLAIN>(g.c, blk, row0, g.m, col, g.n, v);
+          else add_c32<false, PLAIN>(g.c, blk, row0, g.m, col, g.n, v);
         }
         if (epi == kF8EpiRelu2) {
 #pragma unroll
@@ -479,35 +486,48 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
             v[j] = __fmul_rn(__fmul_rn(table[(w[j >> 2] >> (8 * (j & 3))) & 255u], sv_scale), v[j]);
         }
       };
-      // Steps of a tile: 8-bit results take 0 (largest magnitude), 1 (once more over finite
-      // entries, if some entry is infinite) and 2 (codes); dense ones step 2 alone.
+      // the sums of chunk c, finished: the first reading of the accumulator
+      auto first = [&](auto plain, int c, float (&v)[32]) {
+        tmem_ld32(tbase + (uint32_t)(32 * c), v);
+        if (c == shared_c) release_shared();
+        finish(plain, c, v);
+      };
       const bool write_back = epi != kF8EpiNone || add;
+      // ... and the second, of 8-bit results
+      auto again = [&](int c, float (&v)[32]) {
+        if (c == shared_c) {  // the columns may hold the next tile's sums by now
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 x = *reinterpret_cast<const float4*>(keep + lane * 128 + ((q ^ (lane & 7)) << 4));
+            v[4 * q] = x.x; v[4 * q + 1] = x.y; v[4 * q + 2] = x.z; v[4 * q + 3] = x.w;
+          }
+        } else {
+          tmem_ld32(tbase + (uint32_t)(32 * c), v);
+        }
+      };
+      // whole chunks in aligned rows
+      const bool plain_tile = g.out_align >= 16 && col0 + 32 * chunks <= g.n && (!add || g.c.vec);
       float inv = 1.f;
       bool any_inf = false;
+      if (codes_out) {
+        // largest magnitude; finished values wait for the codes
+        auto maximum = [&](auto plain) {
+          float vmax = 0.f;
 #pragma unroll 1
-      for (int step = codes_out ? 0 : 2; step < 3; ++step) {
-        if (step == 1 && !any_inf) continue;
-        float vmax = 0.f;
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          const int c = (k + rot) & 3;
-          if (c >= chunks) {
-            if (backward && (step == 0 || !codes_out)) request_saved((c + 1) & 3);
-            continue;
-          }
-          const int col = col0 + 32 * c;
-          float v[32];
-          if (!codes_out) {
-            tmem_ld32(tbase + (uint32_t)(32 * c), v);
-            if (c == shared_c) release_shared();
-            finish(c, v);
-          } else if (step == 0) {
-            tmem_ld32(tbase + (uint32_t)(32 * c), v);
-            if (c == shared_c) release_shared();
-            finish(c, v);
+          for (int k = 0; k < 4; ++k) {
+            const int c = (k + rot) & 3;
+            if (c >= chunks) {
+              if (backward) request_saved((c + 1) & 3);
+              continue;
+            }
+            float v[32];
+            first(plain, c, v);
             if (c == shared_c) {
               // the other block's warp of this quadrant used the space for the tile before
-              if (it > 0 && !warp_wait(&keep_bar[quad], (uint32_t)((it - 1) & 1))) { ok = false; break; }
+              if (it > 0 && !warp_wait(&keep_bar[quad], (uint32_t)((it - 1) & 1))) {
+                ok = false;
+                break;
+              }
 #pragma unroll
               for (int q = 0; q < 8; ++q)
                 *reinterpret_cast<float4*>(keep + lane * 128 + ((q ^ (lane & 7)) << 4)) =
@@ -515,34 +535,79 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
             } else if (write_back) {
               tmem_st32(tbase + (uint32_t)(32 * c), v);
             }
-          } else if (c == shared_c) {  // the columns may hold the next tile's sums by now
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float4 x = *reinterpret_cast<const float4*>(keep + lane * 128 + ((q ^ (lane & 7)) << 4));
-              v[4 * q] = x.x; v[4 * q + 1] = x.y; v[4 * q + 2] = x.z; v[4 * q + 3] = x.w;
-            }
-          } else {
-            tmem_ld32(tbase + (uint32_t)(32 * c), v);
-          }
-          if (codes_out && step < 2) {
-            const int lim = live ? g.n - col : 0;  // columns that count
-            if (step == 0 && lim >= 32) {
+            if (decltype(plain)::value) {
               float m4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
               for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], fabsf(v[j]));
               vmax = fmaxf(vmax, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
             } else {
+              const int lim = g.n - col0 - 32 * c;  // columns that count
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                vmax = fmaxf(vmax, j >= lim ? 0.f : step == 1 ? f8_finite_abs(v[j]) : fabsf(v[j]));
+              for (int j = 0; j < 32; ++j) vmax = fmaxf(vmax, j < lim ? fabsf(v[j]) : 0.f);
             }
+          }
+          return live ? vmax : 0.f;
+        };
+        // over the block's four warps; a row block is this thread's own row
+        auto over_block = [&](float amax) {
+          if (g.d8.row_blocks) return amax;
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+          float* slot = max_slot + (max_turn & 1) * 8 + half * 4;
+          if (lane == 0) {
+            slot[quad] = amax;
+            mbar_arrive(&max_bar[half]);
+          }
+          ok = warp_wait(&max_bar[half], max_turn & 1u) && ok;
+          ++max_turn;
+          volatile float* sl = slot;
+          return fmaxf(fmaxf(sl[0], sl[1]), fmaxf(sl[2], sl[3]));
+        };
+        float amax = plain_tile ? maximum(std::true_type()) : maximum(std::false_type());
+        if (!ok) break;
+        if (L::kHasSaved) {  // every lane has read the checkpoint: the next tile's may come
+          __syncwarp();
+          request_block(t + n_clusters);
+        }
+        amax = over_block(amax);
+        if (!ok) break;
+        any_inf = __any_sync(0xffffffffu, amax == kF8Inf);
+        if (any_inf) {  // once more over finite entries
+          float vmax = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < chunks; ++c) {
+            float v[32];
+            again(c, v);
+            const int lim = live ? g.n - col0 - 32 * c : 0;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) vmax = fmaxf(vmax, j < lim ? f8_finite_abs(v[j]) : 0.f);
+          }
+          amax = over_block(vmax);
+          if (!ok) break;
+        }
+        const int e = f8_exponent(amax, g.d8.e5m2);
+        inv = f8_exp2(-e);
+        if (live && col0 < g.n && (g.d8.row_blocks || (quad == 0 && lane == 0)))
+          *f8_scale_at(g.d8, row, col0 / kFp8Block) = (uint8_t)(e + 127);
+      }
+
+      // to the result, 32 columns of this thread's row at a time, 32 bytes a store
+      const int parts = codes_out ? 1 : out == kF8OutBf16 ? 2 : 4;
+      uint8_t* const out0 = codes_out ? g.d8.codes : reinterpret_cast<uint8_t*>(g.d.data);
+      const int64_t pitch = codes_out ? g.d8.ld : 2 * (parts / 2) * g.d.ld;
+      uint8_t* const dst0 = out0 + row0 * pitch + (int64_t)col0 * parts;
+      auto emit = [&](auto plain, auto e5m2) {
+        constexpr bool PLAIN = decltype(plain)::value, E5M2 = decltype(e5m2)::value;
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          const int c = (k + rot) & 3;
+          if (c >= chunks) {
+            if (backward && !codes_out) request_saved((c + 1) & 3);
             continue;
           }
-          // 32 columns to the result, 32 bytes of a row at a time
-          const int parts = codes_out ? 1 : out == kF8OutBf16 ? 2 : 4;
-          uint8_t* const out0 = codes_out ? g.d8.codes : reinterpret_cast<uint8_t*>(g.d.data);
-          const int64_t pitch = codes_out ? g.d8.ld : 2 * (parts / 2) * g.d.ld;
-          uint8_t* const dst0 = out0 + row0 * pitch + (int64_t)col * parts;
+          float v[32];
+          if (codes_out) again(c, v);
+          else first(plain, c, v);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             if (i >= parts) break;
@@ -559,20 +624,19 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
             } else {
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                uint2 x;
-                if (g.d8.e5m2) x = f8_encode8<true>(v + 8 * q, inv);
-                else x = f8_encode8<false>(v + 8 * q, inv);
-                if (any_inf)
+                uint2 x = f8_encode8<E5M2>(v + 8 * q, inv);
+                if (!PLAIN && any_inf)
                   x = encode_inf8(make_float4(v[8 * q], v[8 * q + 1], v[8 * q + 2], v[8 * q + 3]),
-                                  make_float4(v[8 * q + 4], v[8 * q + 5], v[8 * q + 6], v[8 * q + 7]), x, g.d8.e5m2);
+                                  make_float4(v[8 * q + 4], v[8 * q + 5], v[8 * q + 6], v[8 * q + 7]), x, E5M2);
                 w[2 * q] = x.x;
                 w[2 * q + 1] = x.y;
               }
             }
-            const int valid = min(32, (g.n - col) * parts - 32 * i);
+            uint8_t* d = dst0 + (int64_t)(32 * c) * parts + 32 * i;
+            const int valid = PLAIN ? 32 : min(32, (g.n - col0 - 32 * c) * parts - 32 * i);
             if (valid <= 0) break;
-            if (valid == 32 && g.out_align >= 16) {
-              uint8_t* d = dst0 + lane * pitch + 32 * i;
+            if (PLAIN || (valid == 32 && g.out_align >= 16)) {
+              d += lane * pitch;
               if (live) {
                 if (g.out_align >= 32) {
                   st_global_32b(d, w);
@@ -584,38 +648,17 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
             } else {
               *block16(blk, lane, 0) = make_uint4(w[0], w[1], w[2], w[3]);
               *block16(blk, lane, 1) = make_uint4(w[4], w[5], w[6], w[7]);
-              rows_from_block(blk, dst0 + 32 * i, pitch, valid, min(32, g.m - row0));
+              rows_from_block(blk, d, pitch, valid, min(32, g.m - row0));
             }
           }
         }
-        if (!ok) break;
-        if (L::kHasSaved && step == 0) {  // every lane has read the checkpoint: the next tile's may come
-          __syncwarp();
-          request_block(t + n_clusters);
-        }
-        if (step == 2) break;
-        // the block's maximum: over this thread's own row, or over the block's four warps
-        float amax = vmax;
-        if (!g.d8.row_blocks) {
-#pragma unroll
-          for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-          float* slot = max_slot + (max_turn & 1) * 8 + half * 4;
-          if (lane == 0) {
-            slot[quad] = amax;
-            mbar_arrive(&max_bar[half]);
-          }
-          if (!warp_wait(&max_bar[half], max_turn & 1u)) { ok = false; break; }
-          ++max_turn;
-          volatile float* sl = slot;
-          amax = fmaxf(fmaxf(sl[0], sl[1]), fmaxf(sl[2], sl[3]));
-        }
-        if (step == 0) any_inf = __any_sync(0xffffffffu, amax == kF8Inf);
-        if (step == 1 || !any_inf) {
-          const int e = f8_exponent(amax, g.d8.e5m2);
-          inv = f8_exp2(-e);
-          if (live && col0 < g.n && (g.d8.row_blocks || (quad == 0 && lane == 0)))
-            *f8_scale_at(g.d8, row, col0 / kFp8Block) = (uint8_t)(e + 127);
-        }
+      };
+      if (codes_out && g.d8.e5m2) {
+        if (plain_tile && !any_inf) emit(std::true_type(), std::true_type());
+        else emit(std::false_type(), std::true_type());
+      } else {
+        if (plain_tile && !any_inf) emit(std::true_type(), std::false_type());
+        else emit(std::false_type(), std::false_type());
       }
       if (!ok) break;
       tc_fence_before();
