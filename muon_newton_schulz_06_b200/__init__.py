@@ -43,7 +43,7 @@ EXPORTED = ("muon_init", "muon_step", "muon_step_ex", "muon_newton_schulz", "muo
             "muon_last_launch_count", "muon_profile_enable", "muon_profile_read", "muon_destroy",
             "muon_status_string", "muon_last_error",
             "muon_fp8_quantize", "muon_fp8_dequantize", "muon_fp8_act_backward", "muon_fp8_matmul",
-            "muon_fp8_profile_read")
+            "muon_fp8_profile_read", "muon_selftest_fp8_timeout")
 
 # muon_kernel_kind
 KERNEL_KINDS = ("momentum_norm", "gram", "poly", "update", "apply", "update_apply", "ns_persistent")
@@ -158,6 +158,8 @@ def load_library(path: str = LIB_PATH):
     lib.muon_fp8_matmul.restype = i32
     lib.muon_fp8_profile_read.argtypes = [vp, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64)]
     lib.muon_fp8_profile_read.restype = i32
+    lib.muon_selftest_fp8_timeout.argtypes = [vp, i64, vp]
+    lib.muon_selftest_fp8_timeout.restype = i32
     lib.muon_destroy.argtypes = [vp]
     lib.muon_destroy.restype = i32
     lib.muon_status_string.argtypes = [i32]
@@ -559,6 +561,12 @@ def muon_fp8_profile_read(handle) -> dict:
     cnt = (ctypes.c_int64 * n)()
     _check(load_library().muon_fp8_profile_read(handle, ms, cnt), handle)
     return {k: (float(ms[i]), int(cnt[i])) for i, k in enumerate(FP8_KERNEL_KINDS)}
+
+
+def muon_selftest_fp8_timeout(handle, limit_ns: int, stream=None) -> None:
+    """Enqueues the time-out diagnostic of the 8-bit products (see include/muon.h); muon_sync
+    then raises MuonError with code MUON_ERR_TIMEOUT."""
+    _check(load_library().muon_selftest_fp8_timeout(handle, int(limit_ns), _stream_ptr(stream, None)), handle)
 
 
 def muon_selftest_wait_timeout(handle, limit_ns: int, stream=None) -> None:

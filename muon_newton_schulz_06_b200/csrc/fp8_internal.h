@@ -152,6 +152,9 @@ struct __align__(64) F8PairParams : F8GemmParamsN<kF8PairProducts> {
 };
 cudaError_t launch_fp8_gemm_pair(const F8PairParams& p, int clusters, cudaStream_t st);
 
+// Diagnostic: the products' bounded wait on a barrier that nothing completes.
+cudaError_t launch_fp8_wait_selftest(int* status, long long limit_clocks, cudaStream_t st);
+
 // 128 x 128 tiles, one CTA each; `split` CTAs (a cluster of 1, 2 or 4) share a tile's
 // contraction and join their sums through distributed shared memory.
 cudaError_t launch_fp8_gemm_tile(const F8GemmParamsN<kF8FewProducts>& p, int split, cudaStream_t st);

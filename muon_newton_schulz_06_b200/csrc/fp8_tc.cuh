@@ -123,19 +123,26 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 constexpr long long kF8WaitClocks = 4000000000ll;  // about 2 s at full clock
-__device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+__device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                           long long limit = kF8WaitClocks) {
   const long long t0 = clock64();
   uint32_t n = 0;
   while (true) {
     if (bar_try(bar, parity)) return true;
     if ((++n & 63u) == 0) {
       if (abort_flag != nullptr && *abort_flag) return false;
-      if (clock64() - t0 > kF8WaitClocks) return false;
+      if (clock64() - t0 > limit) return false;
     }
   }
 }
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   return bar_try(bar, parity) || bar_wait_slow(bar, parity, abort_flag);
+}
+
+// Records a wait that ran out: `status` is a page-locked host word.
+__device__ __forceinline__ void f8_record_timeout(int* status) {
+  *reinterpret_cast<volatile int*>(status) = kDevTimeout;
+  __threadfence_system();
 }
 
 // Arrives on a barrier of either CTA of the pair to hand over tensor memory that has been

@@ -174,8 +174,7 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
   f8_grid_wait();
 
   auto give_up = [&]() {
-    *reinterpret_cast<volatile int*>(p.status) = kDevTimeout;  // page-locked host word
-    __threadfence_system();
+    f8_record_timeout(p.status);
     *abort_flag = 1;
   };
 
@@ -426,6 +425,13 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
   if (split > 1) cluster_sync_all();  // peers have read this CTA's partial tile and maxima
 }
 
+__global__ void fp8_wait_selftest_kernel(int* status, long long limit_clocks) {
+  __shared__ uint64_t bar;
+  mbar_init(&bar, 1);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  if (!bar_wait_slow(smem_u32(&bar), 0, nullptr, limit_clocks)) f8_record_timeout(status);
+}
+
 template <typename Params>
 cudaError_t launch_tile(const Params& p, int split, cudaStream_t st) {
   if (p.total_tiles == 0) return cudaSuccess;
@@ -437,6 +443,11 @@ cudaError_t launch_tile(const Params& p, int split, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t launch_fp8_wait_selftest(int* status, long long limit_clocks, cudaStream_t st) {
+  fp8_wait_selftest_kernel<<<1, 1, 0, st>>>(status, limit_clocks);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_fp8_gemm_tile(const F8GemmParamsN<kF8FewProducts>& p, int split, cudaStream_t st) {
   return launch_tile(p, split, st);

@@ -244,8 +244,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
   f8_grid_wait();
   const uint32_t peer_abort = peer_addr(smem_u32((const void*)abort_flag), rank ^ 1u);
   auto give_up = [&]() {
-    *reinterpret_cast<volatile int*>(p.status) = kDevTimeout;  // page-locked host word
-    __threadfence_system();
+    f8_record_timeout(p.status);
     *abort_flag = 1;
     remote_store_flag(peer_abort, 1);
   };

@@ -56,7 +56,7 @@ struct Call {
     if (!x.data) return fail(h, MUON_ERR_INVALID_ARG, "item %d: %s is NULL", item, what);
     if ((uintptr_t)x.data % (uintptr_t)esz)
       return fail(h, MUON_ERR_INVALID_ARG, "item %d: %s is not aligned to its type", item, what);
-    if (x.ld < x.cols || x.ld > (int64_t(1) << 40))
+    if (x.ld < x.cols || x.ld >= (int64_t(1) << 40))
       return fail(h, MUON_ERR_INVALID_ARG, "item %d: %s has row pitch %lld for %lld columns", item, what,
                   (long long)x.ld, (long long)x.cols);
     add(x.data, x.rows, x.cols * esz, x.ld * esz, written, item);
@@ -75,7 +75,7 @@ struct Call {
     if (!x.codes || !x.scales) return fail(h, MUON_ERR_INVALID_ARG, "item %d: %s has a NULL pointer", item, what);
     if ((uintptr_t)x.codes & 15u)
       return fail(h, MUON_ERR_INVALID_ARG, "item %d: %s has codes that are not 16-byte aligned", item, what);
-    if (x.ld < x.cols || x.ld % 16 || x.ld > (int64_t(1) << 40))
+    if (x.ld < x.cols || x.ld % 16 || x.ld >= (int64_t(1) << 40))
       return fail(h, MUON_ERR_INVALID_ARG, "item %d: %s has row pitch %lld for %lld columns (a multiple of 16)", item,
                   what, (long long)x.ld, (long long)x.cols);
     const int64_t bc = blocks_of(x.cols);
@@ -515,6 +515,22 @@ muon_status muon_fp8_act_backward(muon_handle_t h, const muon_dense* dy, const m
   }
   return run_passes(call, kF8ActBackward, MUON_FP8_KIND_ACT_BACKWARD, passes, act,
                     static_cast<cudaStream_t>(cuda_stream));
+}
+
+muon_status muon_selftest_fp8_timeout(muon_handle_t h, int64_t limit_ns, void* cuda_stream) {
+  if (!h) return MUON_ERR_INVALID_ARG;
+  h->err.clear();
+  if (limit_ns < 0 || limit_ns > 10000000000ll) return fail(h, MUON_ERR_INVALID_ARG, "limit_ns out of range");
+  DeviceGuard dg(h->device);
+  if (!dg.ok) return fail(h, MUON_ERR_CUDA, "cannot select device %d", h->device);
+  muon_status s;
+  if ((s = ensure_fp8(h))) return s;
+  if ((s = poll_status(h, false))) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  const cudaError_t e = launch_fp8_wait_selftest(h->fp8_status_dev, 2 * limit_ns, st);
+  if (e != cudaSuccess) return cuda_fail(h, e, "self-test launch");
+  h->last_launches = 1;
+  return finish_fp8(h, st);
 }
 
 muon_status muon_fp8_matmul(muon_handle_t h, const muon_fp8_product* products, int n, void* cuda_stream) {

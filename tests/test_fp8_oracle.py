@@ -76,6 +76,7 @@ def test_null_handle(lib):
                  lambda: lib.muon_fp8_dequantize(None, None, None, 0, None),
                  lambda: lib.muon_fp8_act_backward(None, None, None, None, None, 0, 0, None),
                  lambda: lib.muon_fp8_matmul(None, None, 0, None),
+                 lambda: lib.muon_selftest_fp8_timeout(None, 0, None),
                  lambda: lib.muon_fp8_profile_read(None, None, None)):
         assert call() == mb.MUON_ERR_INVALID_ARG
 

@@ -4,6 +4,10 @@ backward pass of a relu^2 MLP, gradients into Muon, weights quantised again.
 Every stage is checked against the float64 oracle from the 8-bit matrices that the stage
 itself read, so no bound grows from stage to stage.  A product's accumulation error is taken
 as in test_fp8_matmul.py (ceil(K / 32) + 12 additions, 2^-22 of the sum of magnitudes each)."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -13,6 +17,8 @@ from oracle import fp8
 from test_fp8_blocks import codes, exps, values
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def acc(K):
@@ -139,6 +145,61 @@ def test_gradient_matches_differences():
         dn[i, j] -= 1.0
         assert (loss(up) - loss(dn)) / 2 == dw[i, j].item()
     torch.testing.assert_close(dx, r @ w, rtol=0, atol=0)
+    opt.close()
+
+
+def test_first_calls_of_a_process_can_be_captured():
+    """Kernels that were never launched, and the handle's set-up, inside a capture."""
+    code = """
+import torch, muon_newton_schulz_06_b200 as mb
+x = torch.randn(300, 256, device="cuda")
+w = torch.randn(200, 256, device="cuda")
+big = torch.randn(3000, 256, device="cuda")
+y = torch.empty(300, 200, device="cuda")
+z = torch.empty(3000, 3000, device="cuda", dtype=torch.bfloat16)
+x8, w8, b8 = (mb.Fp8Matrix(*t.shape) for t in (x, w, big))
+d = torch.empty(300, 256, device="cuda")
+g = torch.cuda.CUDAGraph()
+m = mb.Muon(0)
+with torch.cuda.graph(g):
+    m.fp8_quantize([x, w, big], [x8, w8, b8], activation="relu2")
+    m.fp8_act_backward([x], [x8], [d])
+    m.fp8_matmul([mb.Fp8Product(x8, w8, y, trans_b=True)])
+    m.fp8_matmul([mb.Fp8Product(b8, b8, z, trans_b=True)])
+g.replay()
+torch.cuda.synchronize()
+mb.muon_sync(m.handle)
+a, b = (torch.empty_like(t) for t in (x, w))
+m.fp8_dequantize([x8, w8], [a, b])
+ref = a.double() @ b.double().t()
+assert (y.double() - ref).abs().max() <= 1e-5 * ref.abs().max()
+assert torch.equal(z, z.t()) and z.float().abs().sum() > 0
+print("captured", flush=True)
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_time_out_is_reported_and_cleared():
+    opt = mb.Muon(0)
+    mb.muon_selftest_fp8_timeout(opt.handle, 1_000_000)
+    with pytest.raises(mb.MuonError, match="8-bit") as ei:
+        mb.muon_sync(opt.handle)
+    assert ei.value.code == mb.MUON_ERR_TIMEOUT
+    mb.muon_sync(opt.handle)
+    # a later call reports it too, before it enqueues anything; then the handle works on
+    x, m = torch.ones(64, 64, device="cuda"), mb.Fp8Matrix(64, 64)
+    m.codes.fill_(1)
+    mb.muon_selftest_fp8_timeout(opt.handle, 1_000_000)
+    torch.cuda.synchronize()
+    with pytest.raises(mb.MuonError) as ei:
+        opt.fp8_quantize([x], [m])
+    assert ei.value.code == mb.MUON_ERR_TIMEOUT
+    assert (m.codes == 1).all()
+    opt.fp8_quantize([x], [m])
+    assert (values(m) == 1).all()
+    with pytest.raises(mb.MuonError):
+        mb.muon_selftest_fp8_timeout(opt.handle, -1)
     opt.close()
 
 
