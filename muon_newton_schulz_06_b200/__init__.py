@@ -104,6 +104,7 @@ class muon_fp8_product(ctypes.Structure):
 
 
 _lib_handle = None
+_py = None          # the marshalling module of the 8-bit operators
 
 
 def load_library(path: str = LIB_PATH):
@@ -361,7 +362,7 @@ class Fp8Matrix:
     Allocates ``codes`` (uint8, rows padded to a multiple of 16 bytes) and ``scales`` (uint8)
     unless both are given."""
 
-    __slots__ = ("rows", "cols", "format", "blocks", "device", "c", "_codes", "_scales", "_buf")
+    __slots__ = ("rows", "cols", "format", "blocks", "device", "c", "_addr", "_codes", "_scales", "_buf")
 
     def __init__(self, rows: int, cols: int, format: str = "e4m3", blocks: str = "square", device="cuda",
                  codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None):
@@ -401,6 +402,7 @@ class Fp8Matrix:
             # one row has no pitch of its own: any multiple of 16 that holds it will do
             ld = codes.stride(0) if rows > 1 else ld
         self.c = muon_fp8_matrix(p_codes, p_scales, rows, cols, ld, FP8_FORMATS[format], FP8_BLOCKS[blocks])
+        self._addr = ctypes.addressof(self.c)
 
     def _scale_shape(self):
         bc = (self.cols + 127) // 128
@@ -440,29 +442,22 @@ class Fp8Product:
         self.add, self.epilogue, self.saved = add, epilogue, saved
 
 
-def _fp8(m, name: str) -> muon_fp8_matrix:
-    if not isinstance(m, Fp8Matrix):
-        raise TypeError(f"{name} must be an Fp8Matrix")
-    return m.c
-
-
-def _dense(t: torch.Tensor, name: str) -> muon_dense:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    shape = t.shape
-    if len(shape) != 2:
-        raise ValueError(f"{name} must be a 2-D tensor")
-    (rows, cols), (ld, step) = shape, t.stride()
-    if step != 1 and cols > 1 and rows > 0:
-        raise ValueError(f"{name} must have consecutive columns")
-    return muon_dense(t.data_ptr(), rows, cols, ld if rows > 1 else cols, _dtype_code(t))
-
-
-def _list(struct, items, convert, name):
-    """HOST array of the items' structs; a pointer to the one struct for a single item."""
-    if len(items) == 1:
-        return ctypes.byref(convert(items[0], name))
-    return (struct * len(items))(*[convert(t, name) for t in items])
+def _marshal():
+    """The marshalling module (built beside the library), set up on first use."""
+    global _py
+    if _py is None:
+        lib = load_library()
+        try:
+            from . import _muon_py
+        except ImportError as e:
+            raise RuntimeError("_muon_py.so is missing: build it with "
+                               "`python -m muon_newton_schulz_06_b200.build`") from e
+        addresses = tuple(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.muon_fp8_quantize, lib.muon_fp8_dequantize, lib.muon_fp8_act_backward, lib.muon_fp8_matmul))
+        _muon_py.setup(torch.Tensor, torch.bfloat16, torch.float32, Fp8Matrix, Fp8Product, _stream_ptr, FP8_EPILOGUES,
+                       addresses)
+        _py = _muon_py
+    return _py
 
 
 def _activation(act: str) -> int:
@@ -472,35 +467,18 @@ def _activation(act: str) -> int:
     return code
 
 
-def _same_length(names: str, first, *others) -> int:
-    n = len(first)
-    for v in others:
-        if len(v) != n:
-            raise ValueError(f"{names} must have the same length")
-    return n
-
-
 def muon_fp8_quantize(handle, xs: Sequence[torch.Tensor], outs: Sequence[Fp8Matrix], activation: str = "none",
                       stream=None) -> None:
     """outs[i] <- f(xs[i]) in 8 bits (bf16 / fp32 in; f = identity or relu^2): activation
     checkpoints, operands of products, 8-bit copies of weights."""
-    n = _same_length("xs and outs", xs, outs)
-    act = _activation(activation)
-    if n == 0:
-        return
-    x, o = _list(muon_dense, xs, _dense, "x"), _list(muon_fp8_matrix, outs, _fp8, "out")
-    code = load_library().muon_fp8_quantize(handle, x, o, n, act, _stream_ptr(stream, outs[0].device))
+    code = (_py or _marshal()).quantize(handle, xs, outs, _activation(activation), stream)
     if code:
         _check(code, handle)
 
 
 def muon_fp8_dequantize(handle, xs: Sequence[Fp8Matrix], outs: Sequence[torch.Tensor], stream=None) -> None:
     """outs[i] <- the values of xs[i] (bf16 / fp32 out)."""
-    n = _same_length("xs and outs", xs, outs)
-    if n == 0:
-        return
-    x, o = _list(muon_fp8_matrix, xs, _fp8, "x"), _list(muon_dense, outs, _dense, "out")
-    code = load_library().muon_fp8_dequantize(handle, x, o, n, _stream_ptr(stream, xs[0].device))
+    code = (_py or _marshal()).dequantize(handle, xs, outs, stream)
     if code:
         _check(code, handle)
 
@@ -509,46 +487,14 @@ def muon_fp8_act_backward(handle, dys: Sequence[torch.Tensor], saved: Sequence[F
                           activation: str = "relu2", stream=None) -> None:
     """dus[i] <- dys[i] * f'(u) from the checkpoint saved[i] = f(u); each of dus is a tensor
     (which may be dys[i] itself) or an Fp8Matrix."""
-    n = _same_length("dys, saved and dus", dys, saved, dus)
-    act = _activation(activation)
-    if n == 0:
-        return
-    dy, sv = _list(muon_dense, dys, _dense, "dy"), _list(muon_fp8_matrix, saved, _fp8, "saved")
-    du, du8 = (muon_dense * n)(), (muon_fp8_matrix * n)()
-    for i, t in enumerate(dus):
-        if isinstance(t, Fp8Matrix):
-            du8[i] = t.c
-        else:
-            du[i] = _dense(t, "du")
-    code = load_library().muon_fp8_act_backward(handle, dy, sv, du, du8, n, act, _stream_ptr(stream, saved[0].device))
+    code = (_py or _marshal()).act_backward(handle, dys, saved, dus, _activation(activation), stream)
     if code:
         _check(code, handle)
 
 
 def muon_fp8_matmul(handle, products: Sequence[Fp8Product], stream=None) -> None:
     """Runs independent products out = epilogue(add + op(a) op(b)) of 8-bit matrices."""
-    n = len(products)
-    if n == 0:
-        return
-    arr = (muon_fp8_product * n)()
-    for i, p in enumerate(products):
-        q = arr[i]
-        q.a, q.b = _fp8(p.a, "a"), _fp8(p.b, "b")
-        q.trans_a, q.trans_b = (1 if p.trans_a else 0), (1 if p.trans_b else 0)
-        if isinstance(p.out, Fp8Matrix):
-            q.d8 = p.out.c
-        else:
-            q.d = _dense(p.out, "out")
-        if p.add is not None:
-            q.c = _dense(p.add, "add")
-        if p.epilogue not in FP8_EPILOGUES:
-            raise ValueError(f"unknown epilogue {p.epilogue!r}; use one of {sorted(FP8_EPILOGUES)}")
-        q.epilogue = FP8_EPILOGUES[p.epilogue]
-        if (p.saved is not None) != (p.epilogue == "relu2_backward"):
-            raise ValueError("saved belongs to the relu2_backward epilogue, which needs it")
-        if p.saved is not None:
-            q.saved = _fp8(p.saved, "saved")
-    code = load_library().muon_fp8_matmul(handle, arr, n, _stream_ptr(stream, products[0].a.device))
+    code = (_py or _marshal()).matmul(handle, products, stream)
     if code:
         _check(code, handle)
 
@@ -644,7 +590,8 @@ class Muon:
             if len(fp8_params) != len(params):
                 raise ValueError("fp8_params must hold one Fp8Matrix per parameter")
             for i, (m, w) in enumerate(zip(fp8_params, params)):
-                _fp8(m, "fp8_params entry")
+                if not isinstance(m, Fp8Matrix):
+                    raise TypeError(f"fp8_params[{i}] must be an Fp8Matrix")
                 if m.shape != tuple(w.shape):
                     raise ValueError(f"fp8_params[{i}] is {m.shape}, the parameter {tuple(w.shape)}")
         muon_step_ex(self.handle, params, grads, moms, **kw)

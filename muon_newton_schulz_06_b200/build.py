@@ -4,15 +4,19 @@
 
 nvcc compiles every kernel for sm_100a only (tcgen05 / TMA / TMEM instructions) and
 links the CUDA runtime statically, so the library needs no libcudart at load time.
+g++ compiles the binding's marshalling module _muon_py.so (CPython C API).
 """
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmuon_b200.so")
+PY_SOURCE = os.path.join(HERE, "csrc", "muon_py.cpp")
+PY_LIB = os.path.join(HERE, "_muon_py.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -21,10 +25,10 @@ def sources():
 
 
 def up_to_date():
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(PY_LIB):
         return False
-    t = os.path.getmtime(LIB)
-    deps = (sources() + glob.glob(os.path.join(HERE, "csrc", "*.h")) + glob.glob(os.path.join(HERE, "csrc", "*.cuh"))
+    t = min(os.path.getmtime(LIB), os.path.getmtime(PY_LIB))
+    deps = (sources() + [PY_SOURCE] + glob.glob(os.path.join(HERE, "csrc", "*.h")) + glob.glob(os.path.join(HERE, "csrc", "*.cuh"))
             + glob.glob(os.path.join(ROOT, "include", "*.h")))
     return all(os.path.getmtime(d) <= t for d in deps)
 
@@ -40,6 +44,10 @@ def build(verbose_ptxas=False, force=False):
         cmd[1:1] = ["-Xptxas", "-v"]
     subprocess.run(cmd, check=True)
     os.replace(LIB + ".tmp", LIB)
+    subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+                    "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"],
+                    "-o", PY_LIB + ".tmp", PY_SOURCE], check=True)
+    os.replace(PY_LIB + ".tmp", PY_LIB)
     return LIB
 
 
