@@ -20,8 +20,8 @@
 // its partial tile in its shared memory, and each finishes its share of the rows, adding the
 // partial sums in rank order through distributed shared memory.  No workspace, no atomics,
 // one launch, the same sums every time (2048 x 512 x 16384: 30.8 us whole, 20.7 us split in
-// two; bound by the operands' way into shared memory, 128 bytes per clock at the tensor
-// rate against the 50 or so that arrive).
+// two; bound by shared memory, which would have to move 256 bytes per clock at the tensor
+// rate).
 //
 // Every mbarrier wait is bounded; on expiry the kernel writes kDevTimeout to the status
 // word, lets its copies and MMAs drain, frees tensor memory and returns.

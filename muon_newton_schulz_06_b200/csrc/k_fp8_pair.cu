@@ -1,10 +1,13 @@
 // Block-scaled 8-bit products, 256 x 256 tiles by pairs of CTAs (tcgen05 cta_group::2), for
 // results of many tiles.  The formula and the forms are those of k_fp8_gemm.cu.
 //
-// What bounds these products is the operands' way from L2 into shared memory: one SM takes
-// about 50 B/clk (measured here on the 128 x 128 kernel, which asks for 128 B/clk at the
-// tensor rate and stops at 1.7 PFLOP/s), so a CTA has to do more with each byte.  A pair's
-// 256 x 256 tile asks for 64 B/clk per SM.
+// What bounds these products is the operands' way into and out of shared memory. Per k-block of
+// 512 tensor clocks a CTA's share of a 256 x 256 tile writes 32 KB (TMA) and reads 32 KB (MMA),
+// 128 B/clk, all that a shared memory moves; a 128 x 128 tile per CTA needs twice that and stops
+// at 1.8 PFLOP/s. 16384 x 12288 x 4096 takes 606-640 us (2.6-2.7 PFLOP/s, the chip at its power
+// limit), 481 us without copies and epilogue. Not faster: 256 x 224 tiles with two whole
+// accumulators (687 us) and 256 x 384 tiles as instructions of 256 and 128 columns (647 us),
+// which read A twice.
 //
 // Per CTA (384 threads, persistent over the pair's share of the tiles):
 //   warp 0       TMA producer: 6-stage ring of 128 x 128 code tiles of A (this CTA's rows) and
