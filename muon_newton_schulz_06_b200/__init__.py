@@ -379,8 +379,9 @@ class Fp8Matrix:
         self.rows, self.cols, self.format, self.blocks = rows, cols, format, blocks
         if codes is None:
             # one allocation: codes, then scales; the tensors over it are made when asked for
-            n_codes, (sr, sc) = rows * ld, self._scale_shape()
-            buf = torch.empty(n_codes + sr * sc, dtype=torch.uint8, device=device)
+            n_codes, bc = rows * ld, (cols + 127) // 128
+            n_scales = (rows + 127) // 128 * bc if blocks == "square" else bc * rows
+            buf = torch.empty(n_codes + n_scales, dtype=torch.uint8, device=device)
             self._buf, self._codes, self._scales, self.device = buf, None, None, buf.device
             p_codes = buf.data_ptr()
             p_scales = p_codes + n_codes

@@ -125,6 +125,7 @@ struct F8Product {
   int32_t epi;
   int32_t out;             // F8Out
   int32_t out_align;       // largest of 32, 16 that divides the result's base and row pitch in bytes, else 0
+  int32_t seg_kb;          // k-blocks that one accumulation may sum (pair kernel; >= all of them: no segments)
   int32_t tiles_m, tiles_n;
   int32_t tile_begin;      // first tile inside the launch
 };
@@ -146,6 +147,7 @@ static_assert(sizeof(F8GemmParamsN<kMaxF8Products>) <= 32764,
 
 // 256 x 256 tiles by pairs of CTAs, persistent: `clusters` pairs.
 constexpr int kF8PairTile = 256;
+constexpr int32_t kF8SegmentBlocks = 32;  // 4096 of the contraction, a multiple of the 4 of a scale group
 constexpr int kF8PairProducts = 8;
 struct __align__(64) F8PairParams : F8GemmParamsN<kF8PairProducts> {
   CUtensorMap map_saved[kF8PairProducts];  // checkpoints, boxes of 32 rows x 128 codes

@@ -23,6 +23,11 @@
 // two; bound by shared memory, which would have to move 256 bytes per clock at the tensor
 // rate).
 //
+// The tensor cores truncate as they accumulate, so the error grows with the length of a sum:
+// 7e-8 of the result's norm over 4096, 1.2e-6 over 16384.  With the whole tensor memory at
+// hand a contraction longer than 2048 goes to three accumulators, one after another, which the
+// epilogue adds.
+//
 // Every mbarrier wait is bounded; on expiry the kernel writes kDevTimeout to the status
 // word, lets its copies and MMAs drain, frees tensor memory and returns.
 #include "fp8_blocks.cuh"
@@ -39,8 +44,10 @@ constexpr int kTMaxStages = 6;
 constexpr int kTSfSets = 4;  // in shared memory; two in tensor memory
 
 constexpr uint32_t kTSfSet = 2 * kF8SfBytes;   // A words, B words
-constexpr uint32_t kTTmemCols = 256;           // accumulator, then two sets of 8 columns of scales
-constexpr uint32_t kTSfCol = 128;
+// tensor memory: accumulators (one, or three where a CTA has an SM), then two sets of 8 columns
+// of scales
+constexpr int kTAccs = 3;
+__device__ __forceinline__ uint32_t tile_tmem_cols(int accs) { return accs > 1 ? 512u : 256u; }
 constexpr int kTPitch = kT + 4;                // floats per staged row
 static_assert(kT * kTPitch * 4 <= 3 * (int)kTStageBytes, "the staged tile reuses the ring");
 constexpr uint32_t tile_smem(int stages) {
@@ -142,6 +149,10 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
   const int nkb_all = (g.k + kF8K - 1) / kF8K;
   const int per = (nkb_all + split - 1) / split;
   const int kb_begin = min(nkb_all, rank * per), nkb = min(nkb_all, kb_begin + per) - kb_begin;
+  // accumulators: all that fit, those used, and the k-blocks of each
+  const int accs = stages == kTMaxStages ? kTAccs : 1;
+  const int acc_used = min(accs, (nkb + 15) / 16);
+  const int acc_kb = acc_used > 0 ? (nkb + acc_used - 1) / acc_used : 0;
 
   if (g.epi == kF8EpiRelu2Backward) f8_slope_init(slope, g.saved.e5m2, threadIdx.x, kTThreads);
   if (threadIdx.x == 0) {
@@ -163,7 +174,7 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                 "r"(kTTmemCols)
+                 "r"(tile_tmem_cols(accs))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -213,11 +224,13 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
       const uint64_t ring_desc = sdesc(smem_u32(smem), 16, 1024);
       const uint64_t sf_desc = f8_sf_desc(smem_u32(sf_smem));
       uint32_t stage = 0, phase = 0, set = 0, sf_phase = 0, accumulate = 0;
+      uint32_t d_tmem = tmem;
+      int acc_left = acc_kb;
       bool ok = true;
       for (int kb = 0; kb < nkb && ok; kb += kF8Group) {
         // copies and products run in the order of their issue, so the two sets in tensor memory
         // need no barrier of their own
-        const uint32_t sfa = tmem + kTSfCol + (set & 1u) * 8, sfb = sfa + 4;
+        const uint32_t sfa = tmem + 128u * accs + (set & 1u) * 8, sfb = sfa + 4;
         if (!bar_wait(sf_full0 + 8 * set, sf_phase, abort_flag)) { ok = false; break; }
         const uint64_t src = sf_desc + (uint64_t)(set * (kTSfSet >> 4));
         f8_copy_sf(sfa, src);
@@ -230,8 +243,13 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
           const uint32_t id = f8_idesc_sf(idesc, q);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            f8_mma(tmem, ad + k * a_step, bd + k * b_step, id, sfa, sfb, k ? 1u : accumulate);
+            f8_mma(d_tmem, ad + k * a_step, bd + k * b_step, id, sfa, sfb, k ? 1u : accumulate);
           accumulate = 1;
+          if (--acc_left == 0) {  // on to the next accumulator
+            d_tmem += 128;
+            accumulate = 0;
+            acc_left = acc_kb;
+          }
           f8_commit_at(empty0 + 8 * stage);
           if (++stage == stages) { stage = 0; phase ^= 1u; }
         }
@@ -281,7 +299,14 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
     for (int c = 0; c < kChunks; ++c) {
       float v[32];
       if (nkb > 0) {
-        tmem_ld32(tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(32 * kChunks * side + 32 * c), v);
+        const uint32_t at = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(32 * kChunks * side + 32 * c);
+        tmem_ld32(at, v);
+        for (int a = 1; a * acc_kb < nkb; ++a) {
+          float w[32];
+          tmem_ld32(at + 128u * a, w);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] += w[j];
+        }
       } else {
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = 0.f;
@@ -297,7 +322,7 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
   else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTTmemCols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tile_tmem_cols(accs)) : "memory");
   }
 
   // rows rank * 128/split ... of the tile; 16 threads x 8 columns per row

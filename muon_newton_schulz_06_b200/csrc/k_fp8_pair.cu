@@ -31,6 +31,10 @@
 // backward epilogue's checkpoint block comes by TMA, requested a tile ahead (its lookups took
 // 132 us per 8192 x 6144 x 1536 product with loads one chunk ahead and the shared columns in
 // registers).
+// The tensor cores truncate as they accumulate (1.2e-6 of the result's norm over 16384). A
+// float32 result sums at most 4096 in tensor memory: a longer contraction goes tile by tile in
+// segments, each added to what the last one left in the result, by the same thread.
+//
 // Every wait is bounded, the exchange of the maxima included.
 #include <type_traits>
 
@@ -75,6 +79,7 @@ static_assert(kPSfCol + 2 * kPSfCols <= 512, "tensor memory columns");
 
 struct PairTile {
   int gi, row, col, nkb;
+  int seg_kb;  // k-blocks of a segment (a multiple of kF8Group, or all)
 };
 
 // Tiles of a product in bands of 8 tile rows, columns outermost inside a band, so that the
@@ -92,6 +97,7 @@ __device__ __forceinline__ PairTile pair_tile(const Params& p, int t) {
   r.row = (8 * band + rem % h) * kF8PairTile;
   r.col = (rem / h) * kF8PairTile;
   r.nkb = (g.k + kF8K - 1) / kF8K;
+  r.seg_kb = g.seg_kb;
   return r;
 }
 
@@ -174,14 +180,15 @@ __device__ __forceinline__ void add_c32(const F8Dense& c, uint8_t* blk, int row0
   }
 }
 
-// OUT, EPI, ADD: the launch's kind of result, epilogue and addend where every product has the
-// same, -1 otherwise (decided per tile).
+// OUT, EPI: the launch's kind of result and epilogue where every product has the same, -1
+// otherwise (decided per tile).  ADD: 0 where no product has an addend.
 template <typename Params, int OUT, int EPI, int ADD>
 __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   using L = PairSmem<OUT, EPI>;
   constexpr int kPStages8 = L::kStages;
+  constexpr bool kSegments = OUT == kF8OutF32 && EPI == kF8EpiNone && ADD != 0;
   uint8_t* sf_smem = smem + L::sf;
   float* slope = reinterpret_cast<float*>(smem + L::slope);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bars);
@@ -299,48 +306,50 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       const uint32_t sf_full0 = smem_u32(sf_full), sf_empty0 = smem_u32(sf_empty);
       const uint64_t ring_desc = sdesc(smem_u32(smem), 16, 1024);
       const uint64_t sf_desc = f8_sf_desc(smem_u32(sf_smem));
-      for (int t = cluster; t < p.total_tiles && ok; t += n_clusters, ++it) {
+      for (int t = cluster; t < p.total_tiles && ok; t += n_clusters) {
         const PairTile tl = pair_tile(p, t);
         const F8Product& g = p.p[tl.gi];
-        const int acc = it & 1;
         const uint32_t idesc = f8_idesc(g.a_e5m2, g.b_e5m2, g.a_mn, g.b_mn, kF8PairTile, kF8PairTile);
         const uint32_t a_step = (g.a_mn ? 4096 : 32) >> 4, b_step = (g.b_mn ? 4096 : 32) >> 4;
-        if (!bar_wait(smem_u32(&tdone[acc]), (uint32_t)((it >> 1) & 1) ^ 1u, abort_flag) ||
-            (it > 0 && !bar_wait(smem_u32(&tover[acc ^ 1]), (uint32_t)(((it - 1) >> 1) & 1), abort_flag))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem + (uint32_t)acc * kAccStep;
-        uint32_t accumulate = 0;
-        for (int kb = 0; kb < tl.nkb; kb += kF8Group) {
-          // copies and products run in the order of their issue, so the two sets in tensor
-          // memory need no barrier of their own
-          const uint32_t sfa = tmem + kPSfCol + (set & 1u) * kPSfCols, sfb = sfa + 4;
-          if (!bar_wait(sf_full0 + 8 * set, sf_phase, abort_flag)) { ok = false; break; }
-          const uint64_t src = sf_desc + (uint64_t)(set * (kPSfSet >> 4));
-          f8_copy_sf_pair(sfa, src);
-          f8_copy_sf_pair(sfb, src + (kF8SfBytes >> 4));
-          f8_copy_sf_pair(sfb + 4, src + 2 * (kF8SfBytes >> 4));
-          const int n = min(kF8Group, tl.nkb - kb);
+        for (int seg = 0; seg < tl.nkb; seg += tl.seg_kb, ++it) {
+          const int acc = it & 1, seg_end = min(tl.nkb, seg + tl.seg_kb);
+          if (!bar_wait(smem_u32(&tdone[acc]), (uint32_t)((it >> 1) & 1) ^ 1u, abort_flag) ||
+              (it > 0 && !bar_wait(smem_u32(&tover[acc ^ 1]), (uint32_t)(((it - 1) >> 1) & 1), abort_flag))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d_tmem = tmem + (uint32_t)acc * kAccStep;
+          uint32_t accumulate = 0;
+          for (int kb = seg; kb < seg_end; kb += kF8Group) {
+            // copies and products run in the order of their issue, so the two sets in tensor
+            // memory need no barrier of their own
+            const uint32_t sfa = tmem + kPSfCol + (set & 1u) * kPSfCols, sfb = sfa + 4;
+            if (!bar_wait(sf_full0 + 8 * set, sf_phase, abort_flag)) { ok = false; break; }
+            const uint64_t src = sf_desc + (uint64_t)(set * (kPSfSet >> 4));
+            f8_copy_sf_pair(sfa, src);
+            f8_copy_sf_pair(sfb, src + (kF8SfBytes >> 4));
+            f8_copy_sf_pair(sfb + 4, src + 2 * (kF8SfBytes >> 4));
+            const int n = min(kF8Group, seg_end - kb);
 #pragma unroll 1
-          for (int q = 0; q < n; ++q) {
-            if (!bar_wait(full0 + 8 * stage, phase, abort_flag)) { ok = false; break; }
-            const uint64_t ad = ring_desc + (uint64_t)(stage * (kPStage >> 4)), bd = ad + (kPOperand >> 4);
-            const uint32_t id = f8_idesc_sf(idesc, q);
-            f8_mma_pair(d_tmem, ad, bd, id, sfa, sfb, accumulate);
-            accumulate = 1;
+            for (int q = 0; q < n; ++q) {
+              if (!bar_wait(full0 + 8 * stage, phase, abort_flag)) { ok = false; break; }
+              const uint64_t ad = ring_desc + (uint64_t)(stage * (kPStage >> 4)), bd = ad + (kPOperand >> 4);
+              const uint32_t id = f8_idesc_sf(idesc, q);
+              f8_mma_pair(d_tmem, ad, bd, id, sfa, sfb, accumulate);
+              accumulate = 1;
 #pragma unroll
-            for (int k = 1; k < 4; ++k) f8_mma_pair(d_tmem, ad + k * a_step, bd + k * b_step, id, sfa, sfb, 1u);
-            f8_commit_both_at(empty0 + 8 * stage);
-            if (++stage == kPStages8) { stage = 0; phase ^= 1u; }
+              for (int k = 1; k < 4; ++k) f8_mma_pair(d_tmem, ad + k * a_step, bd + k * b_step, id, sfa, sfb, 1u);
+              f8_commit_both_at(empty0 + 8 * stage);
+              if (++stage == kPStages8) { stage = 0; phase ^= 1u; }
+            }
+            if (!ok) break;
+            f8_commit_both_at(sf_empty0 + 8 * set);
+            if (++set == kPSfSets) { set = 0; sf_phase ^= 1u; }
           }
           if (!ok) break;
-          f8_commit_both_at(sf_empty0 + 8 * set);
-          if (++set == kPSfSets) { set = 0; sf_phase ^= 1u; }
+          umma_commit_both(&tfull[acc]);
         }
-        if (!ok) break;
-        umma_commit_both(&tfull[acc]);
       }
       if (!ok) give_up();
       umma_commit_local(drain);
@@ -409,9 +418,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       __syncwarp();
       return got != 0;
     };
-    int it = 0;
+    int it = 0, seg = 0;  // accumulations so far; k-blocks of the tile accumulated before this one
     bool ok = true;
-    for (int t = cluster; t < p.total_tiles && ok; t += n_clusters, ++it) {
+    for (int t = cluster; t < p.total_tiles && ok; ++it) {
       const PairTile tl = pair_tile(p, t);
       const F8Product& g = p.p[tl.gi];
       const int acc = it & 1;
@@ -426,7 +435,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       const bool codes_out = out == kF8OutCodes;
       const int epi = EPI >= 0 ? EPI : g.epi;
       const bool backward = epi == kF8EpiRelu2Backward;
-      const bool add = ADD >= 0 ? ADD != 0 : g.c.data != nullptr;
+      // a later segment adds to the result so far
+      const F8Dense& addend = kSegments && seg > 0 ? g.d : g.c;
+      const bool add = ADD == 0 ? false : addend.data != nullptr;
       const int rot = shared_c == 3 ? 3 : 0;  // the shared chunk comes first
 
       // the checkpoint's codes of this row: in shared memory, or requested one chunk ahead
@@ -468,8 +479,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
         constexpr bool PLAIN = decltype(plain)::value;
         const int col = col0 + 32 * c;
         if (add) {
-          if (g.c.bf16) add_c32<true, PLAIN>(g.c, blk, row0, g.m, col, g.n, v);
-          else add_c32<false, PLAIN>(g.c, blk, row0, g.m, col, g.n, v);
+          if (addend.bf16) add_c32<true, PLAIN>(addend, blk, row0, g.m, col, g.n, v);
+          else add_c32<false, PLAIN>(addend, blk, row0, g.m, col, g.n, v);
         }
         if (epi == kF8EpiRelu2) {
 #pragma unroll
@@ -508,7 +519,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
         }
       };
       // whole chunks in aligned rows
-      const bool plain_tile = g.out_align >= 16 && col0 + 32 * chunks <= g.n && (!add || g.c.vec);
+      const bool plain_tile = g.out_align >= 16 && col0 + 32 * chunks <= g.n && (!add || addend.vec);
       float inv = 1.f;
       bool any_inf = false;
       if (codes_out) {
@@ -667,6 +678,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       __syncwarp();
       if (L::kHasKeep && half == 1 - acc && lane == 0) mbar_arrive(&keep_bar[quad]);
       if (lane == 0) arrive_tmem_free(leader_tdone + (uint32_t)(acc * sizeof(uint64_t)));
+      seg += tl.seg_kb;
+      if (!kSegments || seg >= tl.nkb) {
+        seg = 0;
+        t += n_clusters;
+      }
     }
     if (!ok && lane == 0) {
       give_up();
@@ -702,16 +718,22 @@ cudaError_t launch_fp8_gemm_pair(const F8PairParams& p, int clusters, cudaStream
   using P = F8PairParams;
   if (p.total_tiles == 0) return cudaSuccess;
   const F8Product& g = p.p[0];
+  bool same = true, same_add = true, any_add = false;
+  for (int i = 0; i < p.n; ++i) {
+    const bool add = p.p[i].c.data != nullptr;
+    same = same && p.p[i].out == g.out && p.p[i].epi == g.epi;
+    same_add = same_add && add == (g.c.data != nullptr);
+    any_add = any_add || add || p.p[i].seg_kb < (p.p[i].k + kF8K - 1) / kF8K;
+  }
   const bool add = g.c.data != nullptr;
-  bool same = true;
-  for (int i = 1; i < p.n; ++i)
-    same = same && p.p[i].out == g.out && p.p[i].epi == g.epi && (p.p[i].c.data != nullptr) == add;
+  // (the kernels with an addend do without one where a product has none)
   if (same && g.epi == kF8EpiNone && g.out == kF8OutBf16)
-    return add ? launch_variant<P, kF8OutBf16, kF8EpiNone, 1>(p, clusters, st)
-               : launch_variant<P, kF8OutBf16, kF8EpiNone, 0>(p, clusters, st);
+    return any_add ? launch_variant<P, kF8OutBf16, kF8EpiNone, 1>(p, clusters, st)
+                   : launch_variant<P, kF8OutBf16, kF8EpiNone, 0>(p, clusters, st);
   if (same && g.epi == kF8EpiNone && g.out == kF8OutF32)
-    return add ? launch_variant<P, kF8OutF32, kF8EpiNone, 1>(p, clusters, st)
-               : launch_variant<P, kF8OutF32, kF8EpiNone, 0>(p, clusters, st);
+    return any_add ? launch_variant<P, kF8OutF32, kF8EpiNone, 1>(p, clusters, st)
+                   : launch_variant<P, kF8OutF32, kF8EpiNone, 0>(p, clusters, st);
+  same = same && same_add;
   if (same && g.out == kF8OutCodes && !add) {
     if (g.epi == kF8EpiNone) return launch_variant<P, kF8OutCodes, kF8EpiNone, 0>(p, clusters, st);
     if (g.epi == kF8EpiRelu2) return launch_variant<P, kF8OutCodes, kF8EpiRelu2, 0>(p, clusters, st);

@@ -310,6 +310,8 @@ muon_status fill_products(muon_handle* h, Params& p, const muon_fp8_product* pro
     g.out_align = at % 32 == 0 ? 32 : at % 16 == 0 ? 16 : 0;
     if (q.c.data) g.c = kernel_dense(q.c);
     g.epi = (int32_t)q.epilogue;
+    // only a launch whose results are all float32 without an epilogue goes in segments
+    g.seg_kb = std::max<int32_t>(1, (int32_t)blocks_of(g.k));
     if (q.epilogue == MUON_EPI_RELU2_BACKWARD) {
       g.saved = kernel_fp8(q.saved);
       p.backward = 1;
@@ -334,6 +336,9 @@ muon_status launch_pair_products(muon_handle* h, const muon_fp8_product* product
   if (s) return s;
   for (int i = 0; i < count; ++i)
     if (p.p[i].epi == kF8EpiRelu2Backward && (s = encode_codes(h, &p.map_saved[i], products[live[i]].saved, 32))) return s;
+  bool segments = true;
+  for (int i = 0; i < count; ++i) segments = segments && p.p[i].out == kF8OutF32 && p.p[i].epi == kF8EpiNone;
+  for (int i = 0; i < count && segments; ++i) p.p[i].seg_kb = std::min(p.p[i].seg_kb, kF8SegmentBlocks);
   prof_begin(h, st, kFp8KindBase + MUON_FP8_KIND_MATMUL);
   const cudaError_t e = launch_fp8_gemm_pair(p, (int)std::min<int64_t>(tiles, h->sm_count / 2), st);
   prof_end(h, kFp8KindBase + MUON_FP8_KIND_MATMUL, st);

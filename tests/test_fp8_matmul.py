@@ -273,6 +273,51 @@ def test_launches_of_mixed_kinds(h):
             assert torch.equal(out.cpu(), torch.from_numpy(want).to(out.dtype))
 
 
+@pytest.mark.parametrize("M,N,K", [(2600, 2700, 9001), (257, 300, 16000), (1500, 1400, 5000), (128, 128, 16000)])
+def test_long_contractions_in_parts(h, M, N, K):
+    """float32 results whose contraction is summed in parts: in segments of 4096 that add to the
+    result so far (many tiles), or in several accumulators; with and without an addend, in
+    place, and in rows of odd alignment. Exact, as above (sums stay below 2^20 here)."""
+    for ta, tb in ((False, True), (True, False)):
+        a, b, va, vb = operands(M, N, K, ta, tb, seed=K)
+        want = torch.from_numpy(va).cuda() @ torch.from_numpy(vb).cuda()
+        assert want.abs().max() < 2 ** 20
+        c = torch.randint(-9, 10, (M, N), device="cuda").float()
+        big = torch.full((M, N + 7), 3.0, device="cuda")
+        d, acc = torch.empty(M, N, device="cuda"), c.clone()
+        kw = dict(trans_a=ta, trans_b=tb)
+        mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, d, **kw)])
+        assert torch.equal(d.double(), want)
+        mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, acc, add=acc, **kw)])
+        assert torch.equal(acc.double(), want + c.double())
+        mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, big[:, 3:3 + N], add=c, **kw)])
+        assert torch.equal(big[:, 3:3 + N].double(), want + c.double())
+        assert (big[:, :3] == 3).all() and (big[:, 3 + N:] == 3).all()
+        mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, d, add=c, **kw), mb.Fp8Product(a, b, big[:, :N], **kw)])
+        assert torch.equal(d.double(), want + c.double()) and torch.equal(big[:, :N].double(), want)
+
+
+def test_accuracy_of_long_sums(h):
+    """A contraction of 16384 in parts of 4096 (or less), each n = 128 additions of 32 products.
+    An addition truncates by less than 2^-23 of the partial sum; after i of n random-sign steps
+    that is sqrt(i / n) of the part's result in the mean square, so a part is off by at most
+    2^-23 sqrt(sum i / n) = 2^-23 sqrt((n + 1) / 2) = 9.6e-7 of its result, and four independent
+    parts by the same share of the whole (with 2^-24 for the rounding of their sum: 1.02e-6).
+    Elementwise: n + 12 steps within 2^-22 of the sum of magnitudes, as for every product."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    for M, N in ((4096, 2560), (256, 256)):
+        a, b = mb.Fp8Matrix(16384, M), mb.Fp8Matrix(16384, N)
+        mb.muon_fp8_quantize(h, [torch.randn(16384, n, generator=g, device="cuda") for n in (M, N)], [a, b])
+        va, vb = (torch.empty(16384, n, device="cuda") for n in (M, N))
+        mb.muon_fp8_dequantize(h, [a, b], [va, vb])
+        want = va.double().t() @ vb.double()
+        d = torch.empty(M, N, device="cuda")
+        mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, d, trans_a=True)])
+        err = (d.double() - want)
+        assert err.norm() <= 1.02e-6 * want.norm()
+        assert (err.abs() <= (128 + 12) * 2.0 ** -22 * (va.abs().double().t() @ vb.abs().double())).all()
+
+
 def test_list_of_products_mixed(h):
     """Forms, shapes and destinations mixed in one call; more products than one launch takes;
     empty results and empty contractions among them."""
