@@ -275,8 +275,8 @@ def test_launches_of_mixed_kinds(h):
 
 @pytest.mark.parametrize("M,N,K", [(2600, 2700, 9001), (257, 300, 16000), (1500, 1400, 5000), (128, 128, 16000)])
 def test_long_contractions_in_parts(h, M, N, K):
-    """float32 results whose contraction is summed in parts: in segments of 4096 that add to the
-    result so far (many tiles), or in several accumulators; with and without an addend, in
+    """float32 results whose contraction is summed in parts: in segments of 4096 (many
+    tiles), or in several accumulators; with and without an addend, in
     place, and in rows of odd alignment. Exact, as above (sums stay below 2^20 here)."""
     for ta, tb in ((False, True), (True, False)):
         a, b, va, vb = operands(M, N, K, ta, tb, seed=K)
