@@ -77,7 +77,7 @@ typedef enum {
   MUON_OK = 0,
   MUON_ERR_INVALID_ARG = 1,  /* null / misaligned / overlapping pointers, bad sizes or values */
   MUON_ERR_UNSUPPORTED = 2,  /* a combination the library does not implement (e.g. no sm_100 device) */
-  MUON_ERR_OOM = 3,          /* workspace allocation failed */
+  MUON_ERR_OOM = 3,          /* workspace allocation failed (8-bit operators: host memory ran out) */
   MUON_ERR_CUDA = 4,         /* a CUDA runtime / driver call failed */
   MUON_ERR_TIMEOUT = 5,      /* a bounded device-side wait expired (kernel gave up and returned) */
   MUON_ERR_TOO_LARGE = 6,    /* the matrix does not fit the fixed scratch of muon_newton_schulz_noalloc */

@@ -18,6 +18,9 @@ constexpr int kMaxItems = 65535;
 int64_t blocks_of(int64_t n) { return (n + kFp8Block - 1) / kFp8Block; }
 bool empty(int64_t rows, int64_t cols) { return rows == 0 || cols == 0; }
 
+// rows of `pitch` bytes reach no further than an address space does
+bool addressable(int64_t rows, int64_t pitch) { return pitch <= (int64_t(1) << 47) / rows; }
+
 // One buffer of a call as the overlap check sees it: rows x width bytes at pitch.
 struct Span {
   uintptr_t lo;
@@ -56,7 +59,7 @@ struct Call {
     if (!x.data) return fail(h, MUON_ERR_INVALID_ARG, "item %d: %s is NULL", item, what);
     if ((uintptr_t)x.data % (uintptr_t)esz)
       return fail(h, MUON_ERR_INVALID_ARG, "item %d: %s is not aligned to its type", item, what);
-    if (x.ld < x.cols || x.ld >= (int64_t(1) << 40))
+    if (x.ld < x.cols || x.ld >= (int64_t(1) << 40) || !addressable(x.rows, x.ld * esz))
       return fail(h, MUON_ERR_INVALID_ARG, "item %d: %s has row pitch %lld for %lld columns", item, what,
                   (long long)x.ld, (long long)x.cols);
     add(x.data, x.rows, x.cols * esz, x.ld * esz, written, item);
@@ -75,7 +78,7 @@ struct Call {
     if (!x.codes || !x.scales) return fail(h, MUON_ERR_INVALID_ARG, "item %d: %s has a NULL pointer", item, what);
     if ((uintptr_t)x.codes & 15u)
       return fail(h, MUON_ERR_INVALID_ARG, "item %d: %s has codes that are not 16-byte aligned", item, what);
-    if (x.ld < x.cols || x.ld % 16 || x.ld >= (int64_t(1) << 40))
+    if (x.ld < x.cols || x.ld % 16 || x.ld >= (int64_t(1) << 40) || !addressable(x.rows, x.ld))
       return fail(h, MUON_ERR_INVALID_ARG, "item %d: %s has row pitch %lld for %lld columns (a multiple of 16)", item,
                   what, (long long)x.ld, (long long)x.cols);
     const int64_t bc = blocks_of(x.cols);
@@ -419,12 +422,10 @@ muon_status launch_products(muon_handle* h, const muon_fp8_product* products, co
   return MUON_OK;
 }
 
-}  // namespace
+// ------------------------------------------------------------------ entry points
 
-extern "C" {
-
-muon_status muon_fp8_quantize(muon_handle_t h, const muon_dense* x, const muon_fp8_matrix* out, int n,
-                              muon_activation act, void* cuda_stream) {
+muon_status quantize(muon_handle_t h, const muon_dense* x, const muon_fp8_matrix* out, int n, muon_activation act,
+                     void* cuda_stream) {
   if (!h) return MUON_ERR_INVALID_ARG;
   h->err.clear();
   muon_status s;
@@ -448,8 +449,7 @@ muon_status muon_fp8_quantize(muon_handle_t h, const muon_dense* x, const muon_f
   return run_passes(call, kF8Quantize, MUON_FP8_KIND_QUANTIZE, passes, act, static_cast<cudaStream_t>(cuda_stream));
 }
 
-muon_status muon_fp8_dequantize(muon_handle_t h, const muon_fp8_matrix* x, const muon_dense* out, int n,
-                                void* cuda_stream) {
+muon_status dequantize(muon_handle_t h, const muon_fp8_matrix* x, const muon_dense* out, int n, void* cuda_stream) {
   if (!h) return MUON_ERR_INVALID_ARG;
   h->err.clear();
   muon_status s;
@@ -474,9 +474,8 @@ muon_status muon_fp8_dequantize(muon_handle_t h, const muon_fp8_matrix* x, const
                     static_cast<cudaStream_t>(cuda_stream));
 }
 
-muon_status muon_fp8_act_backward(muon_handle_t h, const muon_dense* dy, const muon_fp8_matrix* saved,
-                                  const muon_dense* du, const muon_fp8_matrix* du8, int n, muon_activation act,
-                                  void* cuda_stream) {
+muon_status act_backward(muon_handle_t h, const muon_dense* dy, const muon_fp8_matrix* saved, const muon_dense* du,
+                         const muon_fp8_matrix* du8, int n, muon_activation act, void* cuda_stream) {
   if (!h) return MUON_ERR_INVALID_ARG;
   h->err.clear();
   muon_status s;
@@ -522,7 +521,7 @@ muon_status muon_fp8_act_backward(muon_handle_t h, const muon_dense* dy, const m
                     static_cast<cudaStream_t>(cuda_stream));
 }
 
-muon_status muon_selftest_fp8_timeout(muon_handle_t h, int64_t limit_ns, void* cuda_stream) {
+muon_status selftest_timeout(muon_handle_t h, int64_t limit_ns, void* cuda_stream) {
   if (!h) return MUON_ERR_INVALID_ARG;
   h->err.clear();
   if (limit_ns < 0 || limit_ns > 10000000000ll) return fail(h, MUON_ERR_INVALID_ARG, "limit_ns out of range");
@@ -538,7 +537,7 @@ muon_status muon_selftest_fp8_timeout(muon_handle_t h, int64_t limit_ns, void* c
   return finish_fp8(h, st);
 }
 
-muon_status muon_fp8_matmul(muon_handle_t h, const muon_fp8_product* products, int n, void* cuda_stream) {
+muon_status matmul(muon_handle_t h, const muon_fp8_product* products, int n, void* cuda_stream) {
   if (!h) return MUON_ERR_INVALID_ARG;
   h->err.clear();
   muon_status s;
@@ -593,6 +592,44 @@ muon_status muon_fp8_matmul(muon_handle_t h, const muon_fp8_product* products, i
   h->last_launches = 0;
   if ((s = launch_products(h, products, live, st))) return s;
   return finish_fp8(h, st);
+}
+
+// No C++ exception (host memory that runs out) crosses the C boundary.
+template <typename F>
+muon_status guarded(F&& f) {
+  try {
+    return f();
+  } catch (...) {
+    return MUON_ERR_OOM;
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+muon_status muon_fp8_quantize(muon_handle_t h, const muon_dense* x, const muon_fp8_matrix* out, int n,
+                              muon_activation act, void* cuda_stream) {
+  return guarded([&] { return quantize(h, x, out, n, act, cuda_stream); });
+}
+
+muon_status muon_fp8_dequantize(muon_handle_t h, const muon_fp8_matrix* x, const muon_dense* out, int n,
+                                void* cuda_stream) {
+  return guarded([&] { return dequantize(h, x, out, n, cuda_stream); });
+}
+
+muon_status muon_fp8_act_backward(muon_handle_t h, const muon_dense* dy, const muon_fp8_matrix* saved,
+                                  const muon_dense* du, const muon_fp8_matrix* du8, int n, muon_activation act,
+                                  void* cuda_stream) {
+  return guarded([&] { return act_backward(h, dy, saved, du, du8, n, act, cuda_stream); });
+}
+
+muon_status muon_fp8_matmul(muon_handle_t h, const muon_fp8_product* products, int n, void* cuda_stream) {
+  return guarded([&] { return matmul(h, products, n, cuda_stream); });
+}
+
+muon_status muon_selftest_fp8_timeout(muon_handle_t h, int64_t limit_ns, void* cuda_stream) {
+  return guarded([&] { return selftest_timeout(h, limit_ns, cuda_stream); });
 }
 
 }  // extern "C"

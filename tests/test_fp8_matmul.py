@@ -391,6 +391,48 @@ def test_deterministic_and_capturable(h):
     mb.muon_destroy(handle)
 
 
+def far(m, pitch):
+    """The same matrix with its rows `pitch` bytes apart (and scales of its own)."""
+    buf = torch.empty(m.rows, pitch, dtype=torch.uint8, device="cuda")
+    buf[:, :m.cols] = m.codes[:, :m.cols]
+    return mb.Fp8Matrix(m.rows, m.cols, format=m.format, blocks=m.blocks, codes=buf[:, :m.cols], scales=m.scales.clone())
+
+
+@pytest.mark.parametrize("N", [1500, 100])
+def test_rows_past_32_bits(h, N):
+    """Operand, checkpoint, addend and results whose last rows lie past 2^32 entries of their
+    base: the same as with rows close together. Pairs (N = 1500) and a CTA per tile."""
+    M, K, pitch = 4100, 256, 1 << 20
+    a, b, _, _ = operands(M, N, K, False, True, seed=9)
+    saved = small_ints(M, N, "e4m3", "row", 11)
+    saved.codes.bitwise_and_(0x7f)                             # a checkpoint of relu^2 is not negative
+    c = torch.randint(-9, 10, (M, N), device="cuda").bfloat16()
+    want, want8 = torch.empty_like(c), mb.Fp8Matrix(M, N)
+    kw = dict(trans_b=True, epilogue="relu2_backward")
+    for out in (want, want8):
+        mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, out, add=c, saved=saved, **kw)])
+    a_far, saved_far, out8 = far(a, pitch), far(saved, pitch), far(want8, pitch)
+    out8.codes.fill_(0)
+    out8.scales.fill_(0)
+    d = torch.empty(M, pitch, dtype=torch.bfloat16, device="cuda")[:, :N]
+    d.copy_(c)
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(a_far, b, out8, add=d, saved=saved_far, **kw)])
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(a_far, b, d, add=d, saved=saved_far, **kw)])
+    assert torch.equal(d, want)
+    assert torch.equal(out8.codes[:, :N], want8.codes[:, :N]) and torch.equal(out8.scales, want8.scales)
+    # the block passes, on the same matrices
+    dy = torch.empty(M, pitch, dtype=torch.bfloat16, device="cuda")[:, :N]
+    mb.muon_fp8_dequantize(h, [out8], [dy])
+    near, du = torch.empty_like(c), torch.empty_like(c)
+    mb.muon_fp8_dequantize(h, [want8], [near])
+    assert torch.equal(dy, near)
+    mb.muon_fp8_act_backward(h, [near], [saved], [du])
+    mb.muon_fp8_act_backward(h, [dy], [saved_far], [d])
+    assert torch.equal(d, du)
+    mb.muon_fp8_quantize(h, [near, dy], [want8, out8])
+    assert torch.equal(out8.codes[:, :N], want8.codes[:, :N]) and torch.equal(out8.scales, want8.scales)
+
+
 def test_refusals(h):
     a, b = mb.Fp8Matrix(64, 128), mb.Fp8Matrix(96, 128)
     d = torch.zeros(64, 96, device="cuda")
@@ -429,3 +471,8 @@ def test_refusals(h):
     assert lib.muon_fp8_matmul(h, raw, 1, None) == mb.MUON_ERR_INVALID_ARG
     assert b"epilogue" in lib.muon_last_error(h)
     mb.muon_sync(h)
+    # rows that no address space holds
+    wide = mb.Fp8Matrix(512, 128)
+    wide.c.ld = 1 << 39
+    with pytest.raises(mb.MuonError, match="pitch"):
+        mb.muon_fp8_dequantize(h, [wide], [torch.empty(512, 128, device="cuda")])
