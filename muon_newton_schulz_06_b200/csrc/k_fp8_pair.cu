@@ -23,7 +23,10 @@
 // Tensor memory holds two accumulators that share 32 columns, [0, 256) and [224, 480), and two
 // sets of scales in the rest: 512 columns have no room for two whole accumulators and scales.
 // The epilogue reads the shared columns first and hands them over; the next tile's MMAs start
-// then and overlap the rest of the epilogue.
+// then and overlap the rest of the epilogue. 8192 x 6144 takes 4.3 us per k-block (11 rounds of
+// tiles) and 16 us whatever its contraction: 6 us of these go without the epilogue (4 of them
+// the stores), the rest are launch, handing over and the last round. Handing the columns over
+// unread changes nothing.
 //
 // An 8-bit result needs its block's maximum before the first code: the four warps of a block
 // read the accumulator twice (maximum; codes). The shared columns wait in shared memory for the
@@ -33,9 +36,9 @@
 // registers).
 // The tensor cores truncate as they accumulate (1.2e-6 of the result's norm over 16384). A
 // float32 result sums at most 4096 in tensor memory: a longer contraction goes tile by tile in
-// segments, and each epilogue thread adds its 128 results up. A segment ends with the same pause
-// for the shared columns as a tile: 6144 x 1536 x 16384 takes 136 us (144 us when each segment
-// went through the result), in bf16 without segments 113 us.
+// segments, which each epilogue thread adds up in 128 registers; the sum goes back to tensor
+// memory for the tile's end, so that nothing there needs the registers (6144 x 1536 x 16384:
+// 125 us; 144 us when each segment went through the result; bf16, without segments, 113-115 us).
 //
 // Every wait is bounded, the exchange of the maxima included.
 #include <type_traits>
@@ -421,19 +424,64 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       __syncwarp();
       return got != 0;
     };
-    int it = 0, seg = 0;  // accumulations so far; k-blocks of the tile accumulated before this one
-    float part[SEG ? 4 : 1][32];  // sum of the tile's segments so far
+    int it = 0;  // accumulations so far
     bool ok = true;
-    for (int t = cluster; t < p.total_tiles && ok; ++it) {
+    for (int t = cluster; t < p.total_tiles && ok; t += n_clusters, ++it) {
       const PairTile tl = pair_tile(p, t);
       const F8Product& g = p.p[tl.gi];
-      const int acc = it & 1;
       const int row0 = tl.row + (int)rank * 128 + 32 * quad, row = row0 + lane;
       const int col0 = tl.col + 128 * half;
       const bool live = row < g.m;
       const int chunks = row0 < g.m ? max(0, min(4, (g.n - col0 + 31) / 32)) : 0;
       // the chunk in the columns shared with the other accumulator, -1 for the other block
-      const int shared_c = acc == 0 ? (half == 1 ? 3 : -1) : (half == 0 ? 0 : -1);
+      auto shared_chunk = [&](int acc) { return acc == 0 ? (half == 1 ? 3 : -1) : (half == 0 ? 0 : -1); };
+      auto columns = [&](int acc) {
+        return tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)acc * kAccStep + (uint32_t)(128 * half);
+      };
+      auto release_shared = [&](int acc) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_tmem_free(leader_tover + (uint32_t)(acc * sizeof(uint64_t)));
+      };
+      if constexpr (SEG) {
+        // the segments before the last one are added up in registers, and their sum to the last
+        // one in tensor memory
+        float part[4][32] = {};
+        for (int seg = tl.seg_kb; ok; seg += tl.seg_kb, ++it) {
+          const int acc = it & 1, shared_c = shared_chunk(acc);
+          const bool last = seg >= tl.nkb;
+          if (!warp_wait(&tfull[acc], (uint32_t)((it >> 1) & 1))) { ok = false; break; }
+          tc_fence_after();
+          if (!last && shared_c >= 0 && shared_c >= chunks) release_shared(acc);
+          auto take = [&](auto chunk) {
+            constexpr int c = decltype(chunk)::value;
+            if (c >= chunks) return;
+            float v[32];
+            tmem_ld32(columns(acc) + (uint32_t)(32 * c), v);
+            if (last) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] += part[c][j];
+              tmem_st32(columns(acc) + (uint32_t)(32 * c), v);
+            } else {
+              if (c == shared_c) release_shared(acc);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) part[c][j] += v[j];
+            }
+          };
+          if (shared_c != 0) take(std::integral_constant<int, 3>());
+          take(std::integral_constant<int, 0>());
+          take(std::integral_constant<int, 1>());
+          take(std::integral_constant<int, 2>());
+          if (shared_c == 0) take(std::integral_constant<int, 3>());
+          if (last) break;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_tmem_free(leader_tdone + (uint32_t)(acc * sizeof(uint64_t)));
+        }
+        if (!ok) break;
+      }
+      const int acc = it & 1;
+      const int shared_c = shared_chunk(acc);
 
       const int out = OUT >= 0 ? OUT : g.out;
       const bool codes_out = out == kF8OutCodes;
@@ -466,35 +514,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       if (!warp_wait(&tfull[acc], (uint32_t)((it >> 1) & 1))) { ok = false; break; }
       if (L::kHasSaved && !warp_wait(&saved_bar[ew], (uint32_t)(it & 1))) { ok = false; break; }
       tc_fence_after();
-      const uint32_t tbase = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)acc * kAccStep + (uint32_t)(128 * half);
-      auto release_shared = [&]() {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_tmem_free(leader_tover + (uint32_t)(acc * sizeof(uint64_t)));
-      };
-      if (shared_c >= 0 && shared_c >= chunks) release_shared();
-      if constexpr (SEG) {
-        auto take = [&](auto chunk) {
-          constexpr int c = decltype(chunk)::value;
-          if (c >= chunks) return;
-          float v[32];
-          tmem_ld32(tbase + (uint32_t)(32 * c), v);
-          if (c == shared_c) release_shared();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) part[c][j] = seg == 0 ? v[j] : part[c][j] + v[j];
-        };
-        if (rot != 0) take(std::integral_constant<int, 3>());
-        take(std::integral_constant<int, 0>());
-        take(std::integral_constant<int, 1>());
-        take(std::integral_constant<int, 2>());
-        if (rot == 0) take(std::integral_constant<int, 3>());
-        // the accumulator is free; the last segment goes on with the sum
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_tmem_free(leader_tdone + (uint32_t)(acc * sizeof(uint64_t)));
-        seg += tl.seg_kb;
-        if (seg < tl.nkb) continue;
-      }
+      const uint32_t tbase = columns(acc);
+      if (shared_c >= 0 && shared_c >= chunks) release_shared(acc);
 
       // addend, activation or its gradient
       // PLAIN: no chunk needs the calls for unaligned rows and edges.  The loops that most
@@ -526,17 +547,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       };
       // the sums of chunk c, finished: the first reading of the accumulator
       auto first = [&](auto plain, int c, float (&v)[32]) {
-        if constexpr (SEG) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i == c) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = part[SEG ? i : 0][j];
-            }
-        } else {
-          tmem_ld32(tbase + (uint32_t)(32 * c), v);
-          if (c == shared_c) release_shared();
-        }
+        tmem_ld32(tbase + (uint32_t)(32 * c), v);
+        if (c == shared_c) release_shared(acc);
         finish(plain, c, v);
       };
       const bool write_back = epi != kF8EpiNone || add;
@@ -708,14 +720,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
         else emit(std::false_type(), std::false_type());
       }
       if (!ok) break;
-      if constexpr (!SEG) {
-        tc_fence_before();
-        __syncwarp();
-        if (L::kHasKeep && half == 1 - acc && lane == 0) mbar_arrive(&keep_bar[quad]);
-        if (lane == 0) arrive_tmem_free(leader_tdone + (uint32_t)(acc * sizeof(uint64_t)));
-      }
-      seg = 0;
-      t += n_clusters;
+      tc_fence_before();
+      __syncwarp();
+      if (L::kHasKeep && half == 1 - acc && lane == 0) mbar_arrive(&keep_bar[quad]);
+      if (lane == 0) arrive_tmem_free(leader_tdone + (uint32_t)(acc * sizeof(uint64_t)));
     }
     if (!ok && lane == 0) {
       give_up();
