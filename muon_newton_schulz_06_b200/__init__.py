@@ -586,7 +586,8 @@ class Muon:
 
     def step(self, params, grads, moms, fp8_params=None, **kw):
         """muon_step_ex; with ``fp8_params`` (list of Fp8Matrix) the updated weights are also
-        quantised into them, on the same stream, for the next forward pass's products."""
+        quantised into them, on the same stream, for the next forward pass's products.
+        Copies that do not fit are refused before the step."""
         if fp8_params is not None:
             if len(fp8_params) != len(params):
                 raise ValueError("fp8_params must hold one Fp8Matrix per parameter")
@@ -595,6 +596,12 @@ class Muon:
                     raise TypeError(f"fp8_params[{i}] must be an Fp8Matrix")
                 if m.shape != tuple(w.shape):
                     raise ValueError(f"fp8_params[{i}] is {m.shape}, the parameter {tuple(w.shape)}")
+                if m.device != w.device:
+                    raise ValueError(f"fp8_params[{i}] is on {m.device}, the parameter on {w.device}")
+                if m.c.codes and (m.c.codes % 16 or m.c.ld % 16):
+                    raise ValueError(f"fp8_params[{i}] needs 16-byte aligned rows")
+            if len({m.c.codes for m in fp8_params if m.c.codes}) < sum(bool(m.c.codes) for m in fp8_params):
+                raise ValueError("fp8_params holds a matrix twice")
         muon_step_ex(self.handle, params, grads, moms, **kw)
         if fp8_params is not None:
             muon_fp8_quantize(self.handle, params, fp8_params, stream=kw.get("stream"))

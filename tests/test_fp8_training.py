@@ -213,5 +213,11 @@ def test_step_refuses_bad_copies_before_stepping():
         opt.step([w], [g], [m], lr=0.1, fp8_params=[mb.Fp8Matrix(64, 65)])
     with pytest.raises(TypeError, match="Fp8Matrix"):
         opt.step([w], [g], [m], lr=0.1, fp8_params=[w])
+    w8 = mb.Fp8Matrix(64, 64)
+    with pytest.raises(ValueError, match="twice"):
+        opt.step([w, w.clone()], [g, g.clone()], [m, m.clone()], lr=0.1, fp8_params=[w8, w8])
+    odd = torch.zeros(64 * 64 + 8, dtype=torch.uint8, device="cuda")[8:].view(64, 64)
+    with pytest.raises(ValueError, match="aligned"):
+        opt.step([w], [g], [m], lr=0.1, fp8_params=[mb.Fp8Matrix(64, 64, codes=odd, scales=w8.scales)])
     assert (w == 1).all() and (m == 0).all()
     opt.close()
