@@ -123,12 +123,13 @@ __device__ __forceinline__ void f8_decode8(uint2 c, float scale, float* v) {
   }
 }
 
-// N groups of 8 consecutive entries of a dense matrix, group i at (row0 + i * step, col):
-// entries outside rows x cols read as 0.  Every load is issued before the first use.
+// N groups of 8 consecutive entries of a dense matrix (here in rows of 16-byte aligned groups),
+// group i at (row0 + i * step, col): entries outside rows x cols read as 0.  Every load is issued
+// before the first use.
 template <int N, bool BF16>
 __device__ __forceinline__ void f8_load_rows_t(const F8Dense& x, int row0, int step, int rows, int col, int cols,
                                                float (&v)[N][8]) {
-  if (x.vec && col + 8 <= cols) {
+  if (col + 8 <= cols) {
     if constexpr (BF16) {
       uint4 raw[N];
       const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(x.data) + (int64_t)row0 * x.ld + col;
@@ -173,64 +174,144 @@ __device__ __forceinline__ void f8_load_rows_t(const F8Dense& x, int row0, int s
     }
   }
 }
+// W words from byte `shift` (even, below 16) of w.
+template <int W>
+__device__ __forceinline__ void f8_shift_words(uint32_t (&w)[W + 4], int shift) {
+  if (shift & 8) {
+#pragma unroll
+    for (int j = 0; j < W + 2; ++j) w[j] = w[j + 2];
+  }
+  if (shift & 4) {
+#pragma unroll
+    for (int j = 0; j < W + 1; ++j) w[j] = w[j + 1];
+  }
+#pragma unroll
+  for (int j = 0; j < W; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], 8 * (shift & 2));
+}
+
+// f8_load_rows for rows whose groups of 8 are not 16-byte aligned: a thread reads the aligned
+// blocks that hold its group (its neighbour reads the shared one too, from the L1 cache) and
+// shifts; groups at a row's ends, whose blocks reach out of the row, go entry by entry.
+// (16384 x 6139 bf16, quantised: 91 us; by 2-byte loads and shared memory 152 us; rows that
+// 16-byte loads can address, 6136 columns: 69 us.)
+template <int N, bool BF16>
+__device__ __forceinline__ void f8_load_rows_shifted(const F8Dense& x, int row0, int step, int rows, int col, int cols,
+                                                     float (&v)[N][8]) {
+  constexpr int kEsz = BF16 ? 2 : 4, kWide = BF16 ? 1 : 2, kWords = 4 * kWide;
+  constexpr int kBatch = BF16 && N > 1 ? 2 : 1;  // rows in flight (more spill)
+  const uint8_t* p0 = reinterpret_cast<const uint8_t*>(x.data) + ((int64_t)row0 * x.ld + col) * kEsz;
+  const int64_t pitch = x.ld * (int64_t)(step * kEsz);
+  const int left = (cols - col) * kEsz;  // bytes to the row's end
+#pragma unroll
+  for (int i0 = 0; i0 < N; i0 += kBatch) {
+    uint32_t w[kBatch][kWords + 4];
+    int shift[kBatch];  // -1: entry by entry
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const uint8_t* p = p0 + (i0 + i) * pitch;
+      const int s = (int)(reinterpret_cast<uintptr_t>(p) & 15u);
+      const bool live = row0 + (i0 + i) * step < rows;
+      const bool whole = s == 0 ? left >= 8 * kEsz : col > 0 && 16 * (kWide + 1) - s <= left;
+      shift[i] = whole ? s : -1;
+      if (whole) {
+        const uint4* q = reinterpret_cast<const uint4*>(p - s);
+#pragma unroll
+        for (int b = 0; b <= kWide; ++b) {
+          const uint4 y = live && (b < kWide || s > 0) ? q[b] : make_uint4(0u, 0u, 0u, 0u);
+          w[i][4 * b] = y.x; w[i][4 * b + 1] = y.y; w[i][4 * b + 2] = y.z; w[i][4 * b + 3] = y.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          w[i][j] = 0u;
+          if (live && j * kEsz < left)
+            w[i][j] = BF16 ? (uint32_t) reinterpret_cast<const uint16_t*>(p)[j] << 16 : reinterpret_cast<const uint32_t*>(p)[j];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (shift[i] >= 0) {
+        f8_shift_words<kWords>(w[i], shift[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[i0 + i][j] =
+              __uint_as_float(!BF16 ? w[i][j % kWords] : j & 1 ? w[i][j / 2] & 0xffff0000u : w[i][j / 2] << 16);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i0 + i][j] = __uint_as_float(w[i][j]);
+      }
+    }
+  }
+}
+
 template <int N>
 __device__ __forceinline__ void f8_load_rows(const F8Dense& x, int row0, int step, int rows, int col, int cols,
                                              float (&v)[N][8]) {
-  if (x.bf16) f8_load_rows_t<N, true>(x, row0, step, rows, col, cols, v);
-  else f8_load_rows_t<N, false>(x, row0, step, rows, col, cols, v);
+  if (x.vec) {
+    if (x.bf16) f8_load_rows_t<N, true>(x, row0, step, rows, col, cols, v);
+    else f8_load_rows_t<N, false>(x, row0, step, rows, col, cols, v);
+  } else {
+    if (x.bf16) f8_load_rows_shifted<N, true>(x, row0, step, rows, col, cols, v);
+    else f8_load_rows_shifted<N, false>(x, row0, step, rows, col, cols, v);
+  }
 }
 
-// Rows whose 8-entry groups are not 16-byte aligned: a half warp moves the 128 entries of
-// a row as 8 runs of 16 and trades them for groups of 8 through `xch`, its 128 floats of
-// shared memory, so that memory sees whole sectors (a thread's own 8 entries one by one
-// cost 43 us against 20 us for storing 4999 x 1531 float32).  Both half warps take part.
-constexpr int kF8Xch = 144;  // floats per half warp: 128, and 16 banks between two of them
+// Stores of such rows: a half warp writes the 128 entries of a row as the aligned 16-byte blocks
+// inside them, and the entries outside whole blocks one per lane (fewer than 8 at either end), by
+// way of `xch`, kF8Xch floats of shared memory. Both half warps take part.  (16384 x 6139 bf16,
+// read back: 77 us; entry by entry through shared memory 108 us; 6136 columns: 58 us.)
+constexpr int kF8Xch = 144;  // floats per half warp: 33 blocks, and 16 banks between two of them
 template <int N, bool BF16>
-__device__ __forceinline__ void f8_load_rows_xch(const F8Dense& x, int row0, int step, int rows, int col, int cols,
-                                                 float (&v)[N][8], float* xch) {
-  const int l = threadIdx.x & 15, c0 = col - 8 * l + l;
+__device__ __forceinline__ void f8_store_rows_xch_t(const F8Dense& x, int row0, int step, int rows, int col, int cols,
+                                                    const float (&v)[N][8], float* xch) {
+  constexpr int kEsz = BF16 ? 2 : 4, kWide = BF16 ? 1 : 2;
+  const int l = threadIdx.x & 15, c0 = col - 8 * l;
+  uint8_t* img = reinterpret_cast<uint8_t*>(xch);  // the entries start 16 bytes into it
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int64_t at = (int64_t)(row0 + i * step) * x.ld + c0;
+    __syncwarp();
+    uint4* own = reinterpret_cast<uint4*>(img + 16 + 16 * kWide * l);
+    if constexpr (BF16) {
+      uint4 raw;
+      __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&raw);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[i][j] = 0.f;
-      if (row0 + i * step < rows && c0 + 16 * j < cols)
-        v[i][j] = BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(x.data)[at + 16 * j])
-                       : reinterpret_cast<const float*>(x.data)[at + 16 * j];
+      for (int j = 0; j < 4; ++j) h[j] = __floats2bfloat162_rn(v[i][2 * j], v[i][2 * j + 1]);
+      own[0] = raw;
+    } else {
+      reinterpret_cast<float4*>(own)[0] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+      reinterpret_cast<float4*>(own)[1] = make_float4(v[i][4], v[i][5], v[i][6], v[i][7]);
     }
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) xch[l + 16 * j] = v[i][j];
     __syncwarp();
-    const float4 a = *reinterpret_cast<const float4*>(xch + 8 * l), b = *reinterpret_cast<const float4*>(xch + 8 * l + 4);
-    v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
-    v[i][4] = b.x; v[i][5] = b.y; v[i][6] = b.z; v[i][7] = b.w;
-    __syncwarp();
+    const bool live = row0 + i * step < rows;
+    // blocks are counted from the aligned address at or below the entries
+    uint8_t* p = reinterpret_cast<uint8_t*>(x.data) + ((int64_t)(row0 + i * step) * x.ld + c0) * kEsz;
+    const int s = (int)(reinterpret_cast<uintptr_t>(p) & 15u), end = s + min(kFp8Block, cols - c0) * kEsz;
+    p -= s;
+    const int hb = s > 0 ? 1 : 0, tb = end >> 4;
+#pragma unroll
+    for (int b = 0; b < kWide; ++b) {
+      const int k = l + 16 * b;
+      // block k holds the entries' bytes from 16 k - s
+      const uint4* q = reinterpret_cast<const uint4*>(img + 16 * (s == 0 ? k + 1 : k));
+      const uint4 y = q[0], z = q[s == 0 ? 0 : 1];
+      uint32_t w[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+      f8_shift_words<4>(w, (16 - s) & 15);
+      if (live && k >= hb && k < tb) *reinterpret_cast<uint4*>(p + 16 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    const int pos = l < 8 ? s + l * kEsz : 16 * tb + (l - 8) * kEsz;
+    if (live && (l < 8 ? hb > 0 && pos < min(16, end) : tb >= hb && pos >= s && pos < end)) {
+      const uint8_t* q = img + 16 + pos - s;
+      if constexpr (BF16) *reinterpret_cast<uint16_t*>(p + pos) = *reinterpret_cast<const uint16_t*>(q);
+      else *reinterpret_cast<uint32_t*>(p + pos) = *reinterpret_cast<const uint32_t*>(q);
+    }
   }
 }
 template <int N>
 __device__ __forceinline__ void f8_store_rows_xch(const F8Dense& x, int row0, int step, int rows, int col, int cols,
                                                   const float (&v)[N][8], float* xch) {
-  const int l = threadIdx.x & 15, c0 = col - 8 * l + l;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    *reinterpret_cast<float4*>(xch + 8 * l) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
-    *reinterpret_cast<float4*>(xch + 8 * l + 4) = make_float4(v[i][4], v[i][5], v[i][6], v[i][7]);
-    __syncwarp();
-    if (row0 + i * step < rows) {
-      const int64_t at = (int64_t)(row0 + i * step) * x.ld + c0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (c0 + 16 * j < cols) {
-          if (x.bf16) reinterpret_cast<__nv_bfloat16*>(x.data)[at + 16 * j] = __float2bfloat16_rn(xch[l + 16 * j]);
-          else reinterpret_cast<float*>(x.data)[at + 16 * j] = xch[l + 16 * j];
-        }
-    }
-    __syncwarp();
-  }
+  if (x.bf16) f8_store_rows_xch_t<N, true>(x, row0, step, rows, col, cols, v, xch);
+  else f8_store_rows_xch_t<N, false>(x, row0, step, rows, col, cols, v, xch);
 }
 
 __device__ __forceinline__ void f8_store8(const F8Dense& x, int64_t row, int col, int cols, const float* v) {

@@ -162,6 +162,37 @@ def test_strided_rows_and_neighbours_left_alone(h):
     assert (out[:, :7] == 9).all() and (out[:, 138:] == 9).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("pitch", [301, 304])
+def test_rows_of_every_alignment(h, dtype, pitch):
+    """Rows that start at any entry, of widths around every edge, between NaN: the bits of the
+    same matrices laid out alone, and nothing beside them written."""
+    rows = 70
+    widths = (1, 3, 7, 8, 9, 17, 127, 128, 129, 134, 135, 136, 137, 250, 256)
+    cases = [(off, c) for off in range(9) for c in widths]
+    xs, alone, near = [], [], []
+    for i, (off, c) in enumerate(cases):
+        base = torch.full((rows, pitch), float("nan"), dtype=DT[dtype], device="cuda")
+        base[:, off:off + c] = data(rows, c, i, dtype).cuda()
+        xs.append(base)
+        near.append(base[:, off:off + c])
+        alone.append(torch.zeros(rows, (c + 15) // 16 * 16, dtype=DT[dtype], device="cuda")[:, :c])
+        alone[-1].copy_(near[-1])
+    ms, refs = [[mb.Fp8Matrix(rows, c) for _, c in cases] for _ in range(2)]
+    mb.muon_fp8_quantize(h, near, ms)
+    mb.muon_fp8_quantize(h, alone, refs)
+    for m, r in zip(ms, refs):
+        assert torch.equal(m.codes[:, :m.cols], r.codes[:, :r.cols]) and torch.equal(m.scales, r.scales)
+    mb.muon_fp8_act_backward(h, near, ms, near)
+    mb.muon_fp8_act_backward(h, alone, refs, alone)
+    for a, b in zip(near, alone):
+        assert torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0))      # the root of a negative entry is NaN
+    mb.muon_fp8_dequantize(h, ms, near)
+    for (off, c), base, m in zip(cases, xs, ms):
+        assert torch.equal(base[:, off:off + c].double().cpu(), torch.from_numpy(values(m)))
+        assert base[:, :off].isnan().all() and base[:, off + c:].isnan().all()
+
+
 def test_empty_and_many(h):
     mb.muon_fp8_quantize(h, [], [])
     z = torch.empty(0, 64, device="cuda")

@@ -225,6 +225,24 @@ def test_every_kind_of_result_of_many_tiles(h, epi, add, saved_fmt, saved_blocks
         assert (out.codes[:, N:] == 0xEE).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(70, 135, 200), (70, 135, 4096), (300, 33, 200)])
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_few_tiles_in_rows_of_every_alignment(h, M, N, K, dt):
+    """Result and addend in rows that start at any entry, whole and split contractions
+    (sums exact in float32, rounded once)."""
+    a, b, va, vb = operands(M, N, K, False, True, seed=M + K)
+    for off in range(9):
+        big = torch.full((M, N + 12), 3.0, dtype=DT[dt], device="cuda")
+        c = torch.full((M, N + 14), float("nan"), dtype=DT[dt], device="cuda")
+        add = c[:, 8 - off:8 - off + N]
+        add.copy_(torch.randint(-9, 10, (M, N), device="cuda"))
+        d = big[:, off:off + N]
+        mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, d, trans_b=True, add=add)])
+        want = torch.from_numpy((va @ vb + add.double().cpu().numpy()).astype(np.float32)).to(DT[dt])
+        assert torch.equal(d.cpu(), want)
+        assert (big[:, :off] == 3).all() and (big[:, off + N:] == 3).all()
+
+
 @pytest.mark.parametrize("M,N,K", [(300, 520, 256), (200, 140, 4096), BIG])
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
 @pytest.mark.parametrize("blocks", ["square", "row"])
