@@ -262,6 +262,30 @@ __device__ __forceinline__ void f8_load_rows(const F8Dense& x, int row0, int ste
 // way of `xch`, kF8Xch floats of shared memory. Both half warps take part.  (16384 x 6139 bf16,
 // read back: 77 us; entry by entry through shared memory 108 us; 6136 columns: 58 us.)
 constexpr int kF8Xch = 144;  // floats per half warp: 33 blocks, and 16 banks between two of them
+// Loads of such float32 rows where nothing else is in registers: 4 bytes per lane, all rows in
+// flight at once, traded for groups of 8 in `xch` (4999 x 1531 quantised and read back: 22.5 us;
+// by aligned blocks, with registers for one row in flight, 26.5).
+template <int N>
+__device__ __forceinline__ void f8_load_rows_xch(const F8Dense& x, int row0, int step, int rows, int col, int cols,
+                                                 float (&v)[N][8], float* xch) {
+  const int l = threadIdx.x & 15, c0 = col - 8 * l + l;
+  const float* p = reinterpret_cast<const float*>(x.data) + (int64_t)row0 * x.ld + c0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[i][j] = row0 + i * step < rows && c0 + 16 * j < cols ? p[(int64_t)(i * step) * x.ld + 16 * j] : 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) xch[l + 16 * j] = v[i][j];
+    __syncwarp();
+    const float4 a = *reinterpret_cast<const float4*>(xch + 8 * l), b = *reinterpret_cast<const float4*>(xch + 8 * l + 4);
+    v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
+    v[i][4] = b.x; v[i][5] = b.y; v[i][6] = b.z; v[i][7] = b.w;
+    __syncwarp();
+  }
+}
 template <int N, bool BF16>
 __device__ __forceinline__ void f8_store_rows_xch_t(const F8Dense& x, int row0, int step, int rows, int col, int cols,
                                                     const float (&v)[N][8], float* xch) {

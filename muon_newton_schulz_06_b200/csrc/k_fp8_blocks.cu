@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(512 / SUB, 2 * SUB) fp8_pass_kernel(const __gr
   constexpr int kThreads = 512 / SUB;
   constexpr int kStep = kThreads / 16;  // rows between a thread's rows
   __shared__ float warp_max[2][kThreads / 32];
-  __shared__ __align__(16) float xch_all[OP == kF8Quantize ? 4 : kThreads / 16 * kF8Xch];
+  __shared__ __align__(16) float xch_all[kThreads / 16 * kF8Xch];
   __shared__ float slope[OP == kF8ActBackward ? kF8SlopeTable : 1];
   const int block = blockIdx.x / SUB;
   int lo = 0, hi = p.n - 1;  // last matrix whose block_begin <= block
@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(512 / SUB, 2 * SUB) fp8_pass_kernel(const __gr
   const int col = bc * kFp8Block + (threadIdx.x & 15) * 8;
   const int row0 = br * kFp8Block + (int)(blockIdx.x % SUB) * (kFp8Block / SUB) + (threadIdx.x >> 4);
 
+  float* xch = xch_all + (threadIdx.x >> 4) * kF8Xch;
   if constexpr (OP == kF8ActBackward) {
     if (p.relu2) {
       f8_slope_init(slope, m.saved.e5m2, threadIdx.x, kThreads);
@@ -82,7 +83,8 @@ __global__ void __launch_bounds__(512 / SUB, 2 * SUB) fp8_pass_kernel(const __gr
       else f8_decode8<false>(c[i], f8_scale(sb[i]), v[i]);
     }
   } else {
-    f8_load_rows<kIter>(m.in, row0, kStep, rows, col, cols, v);
+    if (OP == kF8Quantize && !m.in.vec && !m.in.bf16) f8_load_rows_xch<kIter>(m.in, row0, kStep, rows, col, cols, v, xch);
+    else f8_load_rows<kIter>(m.in, row0, kStep, rows, col, cols, v);
   }
   if constexpr (OP == kF8Quantize) {
     if (p.relu2) {
@@ -102,7 +104,7 @@ __global__ void __launch_bounds__(512 / SUB, 2 * SUB) fp8_pass_kernel(const __gr
       for (int i = 0; i < kIter; ++i)
         if (row0 + i * kStep < rows && col < cols) f8_store8(m.out, row0 + i * kStep, col, cols, v[i]);
     } else {
-      f8_store_rows_xch<kIter>(m.out, row0, kStep, rows, col, cols, v, xch_all + (threadIdx.x >> 4) * kF8Xch);
+      f8_store_rows_xch<kIter>(m.out, row0, kStep, rows, col, cols, v, xch);
     }
     return;
   }
