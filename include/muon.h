@@ -333,7 +333,8 @@ MUON_API muon_status muon_profile_read(muon_handle_t h, double* ms, int64_t* lau
  *
  * Conventions beyond those at the top of this file
  *  - A call takes a list of n independent items (n >= 0); NULL pointers are allowed where
- *    a matrix has no element.  Rows and columns lie in 0 .. 2^24.
+ *    a matrix has no element.  Rows and columns lie in 0 .. 2^24; a matrix's rows span at
+ *    most 2^47 bytes.
  *  - Dense matrices have a row pitch `ld` (elements, >= cols), so a slice of columns of a
  *    larger tensor can be read or written; `data` needs the alignment of its type only
  *    (rows that are 16-byte aligned are moved faster).  Entries outside rows x cols are

@@ -1,6 +1,7 @@
 // Host side of the 8-bit operators: argument checks, kernel parameters and tensor maps,
 // launches.  Nothing is kept between calls but the handle's status word.
 #include <algorithm>
+#include <tuple>
 #include <vector>
 
 #include <nvtx3/nvToolsExt.h>
@@ -90,7 +91,16 @@ struct Call {
 
   // No written buffer may overlap another buffer; every pointer is memory of the device.
   muon_status check() {
-    std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+    std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) {
+      return std::tie(a.lo, a.written, a.rows, a.width, a.pitch) < std::tie(b.lo, b.written, b.rows, b.width, b.pitch);
+    });
+    // an operand that many items read counts once
+    spans.erase(std::unique(spans.begin(), spans.end(),
+                            [](const Span& a, const Span& b) {
+                              return !a.written && !b.written &&
+                                     std::tie(a.lo, a.rows, a.width, a.pitch) == std::tie(b.lo, b.rows, b.width, b.pitch);
+                            }),
+                spans.end());
     for (size_t i = 0; i < spans.size(); ++i)
       for (size_t j = i + 1; j < spans.size() && spans[j].lo < spans[i].hi(); ++j)
         if ((spans[i].written || spans[j].written) && !disjoint_columns(spans[i], spans[j]))

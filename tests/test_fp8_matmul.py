@@ -409,6 +409,19 @@ def test_deterministic_and_capturable(h):
     mb.muon_destroy(handle)
 
 
+def test_many_products_of_one_operand(h):
+    """One weight read by every item of a long list, each with a result of its own."""
+    n = 20000
+    w = small_ints(40, 160, "e4m3", "square", 1)
+    x = small_ints(3, 160, "e4m3", "row", 2)
+    y = torch.full((n, 3, 40), 7.0, device="cuda")
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(x, w, y[i], trans_b=True) for i in range(n)])
+    want = torch.from_numpy(values(x) @ values(w).T).float().cuda()
+    assert (y == want).all()
+    with pytest.raises(mb.MuonError, match="overlap"):                 # two of them to one result
+        mb.muon_fp8_matmul(h, [mb.Fp8Product(x, w, y[i % (n - 1)], trans_b=True) for i in range(n)])
+
+
 def far(m, pitch):
     """The same matrix with its rows `pitch` bytes apart (and scales of its own)."""
     buf = torch.empty(m.rows, pitch, dtype=torch.uint8, device="cuda")
