@@ -409,6 +409,29 @@ def test_deterministic_and_capturable(h):
     mb.muon_destroy(handle)
 
 
+@pytest.mark.parametrize("ta,tb", [(False, True), (False, False), (True, False), (True, True)])
+@pytest.mark.parametrize("M,N,K", [(2048, 512, 4200), (1000, 1400, 2100), (1013, 777, 4100), (130, 2200, 5000),
+                                   (640, 1290, 4096), (1500, 1025, 8000)])
+def test_exact_mid_sizes_with_long_contractions(h, M, N, K, ta, tb):
+    """Results of 36 to 148 tiles of 128 x 128, contractions whole and split; dense epilogues,
+    addends, rows of any alignment."""
+    a, b, va, vb = operands(M, N, K, ta, tb, seed=M + K)
+    base = torch.from_numpy(va).cuda() @ torch.from_numpy(vb).cuda()
+    kw = dict(trans_a=ta, trans_b=tb)
+    for dt, pad, off in (("fp32", 0, 0), ("bf16", 0, 0), ("fp32", 7, 3), ("bf16", 7, 5)):
+        c = torch.randint(-9, 10, (M, N), device="cuda").to(DT[dt])
+        big = torch.full((M, N + pad), 3.0, dtype=DT[dt], device="cuda")
+        d = big[:, off:off + N]
+        mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, d, **kw)])
+        assert torch.equal(d, base.float().to(DT[dt]))
+        mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, d, add=c, epilogue="relu2", **kw)])
+        assert torch.equal(d, (base + c.double()).float().relu().square().to(DT[dt]))
+        acc = c.clone()                                                   # two in one launch, one in place
+        mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, d, add=c, **kw), mb.Fp8Product(a, b, acc, add=acc, **kw)])
+        assert torch.equal(d, (base + c.double()).float().to(DT[dt])) and torch.equal(d, acc)
+        assert (big[:, :off] == 3).all() and (big[:, off + N:] == 3).all()
+
+
 def test_many_products_of_one_operand(h):
     """One weight read by every item of a long list, each with a result of its own."""
     n = 20000
