@@ -508,7 +508,7 @@ muon_status act_backward(muon_handle_t h, const muon_dense* dy, const muon_fp8_m
     if (to_dense) {
       if (du[i].rows != rows || du[i].cols != cols)
         return fail(h, MUON_ERR_INVALID_ARG, "item %d: dy and du differ in shape", i);
-      // in place: every entry is read and written by the same thread
+      // in place: the warp that writes an entry has read it before
       if (!same_dense(dy[i], du[i]) && (s = call.dense(dy[i], "dy", i, false))) return s;
       if ((s = call.dense(du[i], "du", i, true))) return s;
     } else {
@@ -585,7 +585,7 @@ muon_status matmul(muon_handle_t h, const muon_fp8_product* products, int n, voi
       if (q.c.rows != m || q.c.cols != nn)
         return fail(h, MUON_ERR_INVALID_ARG, "item %d: c is %lld x %lld, the product %lld x %lld", i,
                     (long long)q.c.rows, (long long)q.c.cols, (long long)m, (long long)nn);
-      // c = d: every entry is read and written by the same thread
+      // c = d: the warp that writes an entry has read it before
       if (!(to_dense && same_dense(q.c, q.d)) && (s = call.dense(q.c, "c", i, false))) return s;
     }
     if (q.epilogue == MUON_EPI_RELU2_BACKWARD) {
