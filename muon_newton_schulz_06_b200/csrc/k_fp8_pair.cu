@@ -743,7 +743,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       if (!ok) break;
       tc_fence_before();
       __syncwarp();
-      if (L::kHasKeep && half == 1 - acc && lane == 0) mbar_arrive(&keep_bar[quad]);
+      if (L::kHasKeep && half == 1 - acc) {
+        // Tiles hand the space over in order: a warp that had no use for it (a dense result, or a
+        // chunk past the edge) still waits for the tile before. An arrival ahead of the other
+        // block's would complete two phases, and the wait for the first of them would not end.
+        if (it > 0 && !warp_wait(&keep_bar[quad], (uint32_t)((it - 1) & 1))) { ok = false; break; }
+        if (lane == 0) mbar_arrive(&keep_bar[quad]);
+      }
       if (lane == 0) arrive_tmem_free(leader_tdone + (uint32_t)(acc * sizeof(uint64_t)));
     }
     if (!ok && lane == 0) {
