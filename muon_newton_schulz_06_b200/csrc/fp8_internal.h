@@ -12,6 +12,18 @@ namespace muon {
 
 constexpr int kFp8Block = 128;
 
+// The four bytes at `at` of a buffer [lo, hi), read as the aligned words that hold them, or one
+// by one where such a word would reach out of the buffer (at its two ends, when it does not start
+// or end at a multiple of four). word(a), byte(a): the reads.
+template <typename Word, typename Byte>
+__host__ __device__ __forceinline__ uint32_t f8_read4(uintptr_t at, uintptr_t lo, uintptr_t hi, Word word, Byte byte) {
+  const uint32_t off = (uint32_t)(at & 3u);
+  if (off == 0) return word(at);
+  const uintptr_t first = at - off;
+  if (first >= lo && first + 8 <= hi) return word(first) >> (8 * off) | word(first + 4) << (32 - 8 * off);
+  return byte(at) | byte(at + 1) << 8 | byte(at + 2) << 16 | byte(at + 3) << 24;
+}
+
 // Launch of one of these kernels: `cluster` CTAs per cluster, and its start may overlap the
 // end of the kernel before it on the stream (programmatic stream serialization).  Every
 // kernel here lets the next one start as soon as all its CTAs run, and touches memory only

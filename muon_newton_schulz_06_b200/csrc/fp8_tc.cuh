@@ -181,7 +181,7 @@ __device__ __forceinline__ bool elect_one() {
 // k-blocks out of range take 2^0 (their codes are zero).  f8_sf_load issues the loads,
 // f8_sf_store puts the words where the copy to tensor memory expects them (512 bytes at dst).
 // Lane l has rows l + 32 j, or, where all 128 rows exist (`quads`), rows 4 l + j: their four
-// bytes lie together, in one aligned word or two, in the place of four loads.
+// bytes lie together, in one aligned word or two, in the place of four loads (f8_read4).
 struct F8SfWords {
   uint32_t w[4];
   bool quads;
@@ -202,13 +202,15 @@ __device__ __forceinline__ F8SfWords f8_sf_load(const F8Scales& s, int r0, int r
   f.quads = r0 + kFp8Block <= rows;
   if (f.quads) {
     uint32_t x[4];
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(s.s), hi = lo + (uintptr_t)((int64_t)nkb * s.s_k);
 #pragma unroll
     for (int q = 0; q < kF8Group; ++q) {
-      const uint8_t* at = p + (int64_t)q * s.s_k + 4 * lane;
-      const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(at) & 3u);  // the same in all lanes
-      const uint32_t* word = reinterpret_cast<const uint32_t*>(at - off);
       x[q] = 0x7f7f7f7fu;
-      if (kb0 + q < nkb) x[q] = off == 0 ? word[0] : __funnelshift_r(word[0], word[1], 8 * off);
+      if (kb0 + q < nkb)
+        x[q] = f8_read4(
+            reinterpret_cast<uintptr_t>(p + (int64_t)q * s.s_k + 4 * lane), lo, hi,
+            [](uintptr_t a) { return *reinterpret_cast<const uint32_t*>(a); },
+            [](uintptr_t a) { return (uint32_t)*reinterpret_cast<const uint8_t*>(a); });
     }
     // byte j of the four loads makes row j's word
     const uint32_t a = __byte_perm(x[0], x[1], 0x5140), b = __byte_perm(x[2], x[3], 0x5140);
