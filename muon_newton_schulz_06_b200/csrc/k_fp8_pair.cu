@@ -167,6 +167,15 @@ __device__ __noinline__ uint2 encode_inf8(float4 a, float4 b, uint2 c, bool e5m2
   return e5m2 ? f8_encode_inf8<true>(v, c) : f8_encode_inf8<false>(v, c);
 }
 
+// The n codes at q (16-byte aligned) that lie before the row's end, at most 16.
+__device__ __noinline__ uint4 codes_edge(const uint8_t* q, int n) {
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (j < n) w[j >> 2] |= (uint32_t)q[j] << (8 * (j & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // 32 consecutive entries of this thread's row of the addend (row0 + lane, col ..).
 // VEC: whole 32 columns in rows that 16-byte loads can address.
 template <bool BF16, bool VEC>
@@ -519,9 +528,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
         if (L::kHasSaved) return;
         const uint8_t* q = g.saved.codes + (int64_t)row * g.saved.ld + col0 + 32 * c;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          sv_next[i] = live && col0 + 32 * c + 16 * i < g.n ? *reinterpret_cast<const uint4*>(q + 16 * i)
-                                                            : make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < 2; ++i) {
+          const int left = live ? g.n - (col0 + 32 * c + 16 * i) : 0;
+          sv_next[i] = left >= 16 ? *reinterpret_cast<const uint4*>(q + 16 * i)
+                       : left > 0 ? codes_edge(q + 16 * i, left)
+                                  : make_uint4(0u, 0u, 0u, 0u);
+        }
       };
       if (backward) {
         request_saved(rot);

@@ -83,3 +83,28 @@ def test_row_scales_at_any_address(M, N, K, lead):
     mb.muon_sync(h)
     assert torch.equal(d.double(), torch.from_numpy(va).cuda() @ torch.from_numpy(vb).cuda())
     mb.muon_destroy(h)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [2305, 2319, 2177])
+def test_checkpoint_that_ends_with_its_last_entry(N):
+    """The slope epilogue into dense results, many tiles: the last row's codes are the last bytes
+    of their buffer."""
+    import muon_newton_schulz_06_b200 as mb
+    from oracle import fp8
+    from test_fp8_blocks import values
+    from test_fp8_matmul import operands, roots
+    h = mb.muon_init(0)
+    M, K, ld = 2437, 200, (N + 15) // 16 * 16
+    a, b, va, vb = operands(M, N, K, False, True, seed=N)
+    whole = roots(M, N, "e4m3", "square", 3)
+    buf = torch.empty((M - 1) * ld + N, dtype=torch.uint8, device="cuda")
+    codes = buf.as_strided((M, N), (ld, 1))
+    codes.copy_(whole.codes[:, :N])
+    saved = mb.Fp8Matrix(M, N, codes=codes, scales=whole.scales)
+    d = torch.empty(M, N, device="cuda")
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, d, trans_b=True, epilogue="relu2_backward", saved=saved)])
+    mb.muon_sync(h)
+    want = torch.from_numpy(fp8.relu2_backward(va @ vb, values(whole)))
+    assert torch.equal(d.double().cpu(), want.float().double())
+    mb.muon_destroy(h)
