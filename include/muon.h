@@ -439,9 +439,10 @@ typedef enum {
  * Products of codes are exact, scales are powers of two, sums are fp32 in tensor memory.
  * The tensor cores truncate there, so the error grows with the length of a sum: on normal
  * data 6e-8 of the result's norm at 1024, 2.2e-7 at 4096, 1.2e-6 at 16384.  Float32 results
- * without an epilogue are therefore summed in parts of about 4096, joined in float32 with
- * rounding to nearest (2.2e-7 at K = 16384, 3e-7 at 65536); the others' rounding is far
- * larger.  The epilogue works in float32 and rounds once.  A K of 0 gives epi(C). */
+ * without an epilogue are therefore summed in parts of at most 4096, joined in float32 with
+ * rounding to nearest (2.2e-7 at K = 16384, 2.3e-7 at 65536), in every list and size; float32
+ * results with one and 16- or 8-bit ones, whose rounding is far larger, may be summed in one
+ * piece.  The epilogue works in float32 and rounds once.  A K of 0 gives epi(C). */
 typedef struct {
   muon_fp8_matrix a;
   muon_fp8_matrix b;

@@ -157,9 +157,13 @@ struct __align__(64) F8GemmParamsN {
 static_assert(sizeof(F8GemmParamsN<kMaxF8Products>) <= 32764,
               "parameters of the 8-bit products must fit the kernel parameter space");
 
+// A float32 result sums this many k-blocks at most in tensor memory (4096 of the contraction; a
+// multiple of the 4 of a scale group).
+constexpr int32_t kF8SegmentBlocks = 32;
+constexpr int32_t kF8TileAccs = 3;  // accumulators of a 128 x 128 tile with an SM of its own
+
 // 256 x 256 tiles by pairs of CTAs, persistent: `clusters` pairs.
 constexpr int kF8PairTile = 256;
-constexpr int32_t kF8SegmentBlocks = 32;  // 4096 of the contraction, a multiple of the 4 of a scale group
 constexpr int kF8PairProducts = 8;
 struct __align__(64) F8PairParams : F8GemmParamsN<kF8PairProducts> {
   CUtensorMap map_saved[kF8PairProducts];  // checkpoints, boxes of 32 rows x 128 codes
@@ -170,8 +174,9 @@ cudaError_t launch_fp8_gemm_pair(const F8PairParams& p, int clusters, cudaStream
 cudaError_t launch_fp8_wait_selftest(int* status, long long limit_clocks, cudaStream_t st);
 
 // 128 x 128 tiles, one CTA each; `split` CTAs (a cluster of 1, 2 or 4) share a tile's
-// contraction and join their sums through distributed shared memory.
-cudaError_t launch_fp8_gemm_tile(const F8GemmParamsN<kF8FewProducts>& p, int split, cudaStream_t st);
-cudaError_t launch_fp8_gemm_tile(const F8GemmParamsN<kMaxF8Products>& p, int split, cudaStream_t st);
+// contraction and join their sums through distributed shared memory.  segments: shares longer
+// than the accumulators' kF8TileAccs * kF8SegmentBlocks are summed in segments (six stages only).
+cudaError_t launch_fp8_gemm_tile(const F8GemmParamsN<kF8FewProducts>& p, int split, bool segments, cudaStream_t st);
+cudaError_t launch_fp8_gemm_tile(const F8GemmParamsN<kMaxF8Products>& p, int split, bool segments, cudaStream_t st);
 
 }  // namespace muon

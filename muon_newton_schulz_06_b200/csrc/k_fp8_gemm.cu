@@ -24,9 +24,11 @@
 // rate).
 //
 // The tensor cores truncate as they accumulate, so the error grows with the length of a sum:
-// 7e-8 of the result's norm over 4096, 1.2e-6 over 16384.  With the whole tensor memory at
-// hand a contraction longer than 2048 goes to three accumulators, one after another, which the
-// epilogue adds.
+// 2.2e-7 of the result's norm over 4096, 1.2e-6 over 16384.  With the whole tensor memory at
+// hand a CTA's share of the contraction goes to up to three accumulators, one per 2048, one after
+// another, which the epilogue adds.  A float32 result may sum 4096 at most in one of them: where
+// its share is longer than three of these (SEG), the three take segments of 4096 in turn, and the
+// warps without a part in the loop above add each to a sum in registers while the next one runs.
 //
 // Every mbarrier wait is bounded; on expiry the kernel writes kDevTimeout to the status
 // word, lets its copies and MMAs drain, frees tensor memory and returns.
@@ -46,7 +48,7 @@ constexpr int kTSfSets = 4;  // in shared memory; two in tensor memory
 constexpr uint32_t kTSfSet = 2 * kF8SfBytes;   // A words, B words
 // tensor memory: accumulators (one, or three where a CTA has an SM), then two sets of 8 columns
 // of scales
-constexpr int kTAccs = 3;
+constexpr int kTAccs = kF8TileAccs;
 __device__ __forceinline__ uint32_t tile_tmem_cols(int accs) { return accs > 1 ? 512u : 256u; }
 constexpr int kTPitch = kT + 4;                // floats per staged row
 static_assert(kT * kTPitch * 4 <= 3 * (int)kTStageBytes, "the staged tile reuses the ring");
@@ -118,8 +120,9 @@ __device__ __forceinline__ void fetch_split(uint32_t addr, float* v) {
   }
 }
 
-template <typename Params>
-__global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_constant__ Params p) {
+// SEG: segments as above, one CTA per SM.
+template <typename Params, bool SEG>
+__global__ void __launch_bounds__(kTThreads, SEG ? 1 : 2) fp8_tile_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t stages = (uint32_t)p.stages;
@@ -130,7 +133,9 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
   uint64_t* sf_full = empty + kTMaxStages;
   uint64_t* sf_empty = sf_full + kTSfSets;
   uint64_t* done = sf_empty + kTSfSets;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* seg_full = done + 1;            // [kTAccs] a segment is summed
+  uint64_t* seg_free = seg_full + kTAccs;   // [kTAccs] and has been read
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(seg_free + kTAccs);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* cta_max = reinterpret_cast<float*>(tmem_slot + 2);  // this CTA's maximum
   float* warp_max = cta_max + 1;                             // [8]
@@ -150,7 +155,7 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
   const int per = (nkb_all + split - 1) / split;
   const int kb_begin = min(nkb_all, rank * per), nkb = min(nkb_all, kb_begin + per) - kb_begin;
   // accumulators: all that fit, those used, and the k-blocks of each
-  const int accs = stages == kTMaxStages ? kTAccs : 1;
+  const int accs = SEG || stages == kTMaxStages ? kTAccs : 1;
   const int acc_used = min(accs, (nkb + 15) / 16);
   const int acc_kb = acc_used > 0 ? (nkb + acc_used - 1) / acc_used : 0;
 
@@ -165,6 +170,10 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
       mbar_init(&sf_empty[s], 1);
     }
     mbar_init(done, 1);
+    for (int a = 0; SEG && a < kTAccs; ++a) {
+      mbar_init(&seg_full[a], 1);
+      mbar_init(&seg_free[a], 4);
+    }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -226,8 +235,15 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
       uint32_t stage = 0, phase = 0, set = 0, sf_phase = 0, accumulate = 0;
       uint32_t d_tmem = tmem;
       int acc_left = acc_kb;
+      uint32_t seg_acc = 0, seg_phase = 1;
       bool ok = true;
       for (int kb = 0; kb < nkb && ok; kb += kF8Group) {
+        if (SEG && kb % kF8SegmentBlocks == 0) {
+          if (!bar_wait(smem_u32(&seg_free[seg_acc]), seg_phase, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          d_tmem = tmem + 128 * seg_acc;
+          accumulate = 0;
+        }
         // copies and products run in the order of their issue, so the two sets in tensor memory
         // need no barrier of their own
         const uint32_t sfa = tmem + 128u * accs + (set & 1u) * 8, sfb = sfa + 4;
@@ -245,13 +261,17 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
           for (int k = 0; k < 4; ++k)
             f8_mma(d_tmem, ad + k * a_step, bd + k * b_step, id, sfa, sfb, k ? 1u : accumulate);
           accumulate = 1;
-          if (--acc_left == 0) {  // on to the next accumulator
+          if (!SEG && --acc_left == 0) {  // on to the next accumulator
             d_tmem += 128;
             accumulate = 0;
             acc_left = acc_kb;
           }
           f8_commit_at(empty0 + 8 * stage);
           if (++stage == stages) { stage = 0; phase ^= 1u; }
+        }
+        if (SEG && ok && ((kb + kF8Group) % kF8SegmentBlocks == 0 || kb + kF8Group >= nkb)) {
+          f8_commit_at(smem_u32(&seg_full[seg_acc]));
+          if (++seg_acc == kTAccs) { seg_acc = 0; seg_phase ^= 1u; }
         }
         f8_commit_at(sf_empty0 + 8 * set);
         if (++set == kTSfSets) { set = 0; sf_phase ^= 1u; }
@@ -284,6 +304,39 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
     }
   }
 
+  // warps 4 to 7: the segments' sum of row 32 (warp % 4) + lane
+  float part[SEG ? 4 : 1][32];
+  if constexpr (SEG) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int j = 0; j < 32; ++j) part[c][j] = 0.f;
+    if (warp >= 4) {
+      uint32_t acc = 0, phase = 0;
+      for (int seg = 0; seg < nkb; seg += kF8SegmentBlocks) {
+        int ok = 1;
+        if (lane == 0) ok = bar_wait(smem_u32(&seg_full[acc]), phase, abort_flag);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) {
+          if (lane == 0) give_up();
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float v[32];
+          tmem_ld32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 128u * acc + 32u * c, v);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) part[c][j] += v[j];
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_free[acc]);
+        if (++acc == kTAccs) { acc = 0; phase ^= 1u; }
+      }
+    }
+  }
+
   // the accumulator is final and the ring free once `done` completes
   if (lane == 0) (void)bar_wait(smem_u32(done), 0, nullptr);
   __syncwarp();
@@ -291,7 +344,17 @@ __global__ void __launch_bounds__(kTThreads, 2) fp8_tile_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   float* stage_f = reinterpret_cast<float*>(smem);
-  {
+  if constexpr (SEG) {
+    if (warp >= 4) {
+      float* dst = stage_f + (32 * (warp & 3) + lane) * kTPitch;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<float4*>(dst + 32 * c + 4 * j) =
+              make_float4(part[c][4 * j], part[c][4 * j + 1], part[c][4 * j + 2], part[c][4 * j + 3]);
+    }
+  } else {
     const int quad = warp & 3, side = warp >> 2;
     constexpr int kChunks = 2;  // 32 columns each
     float* dst = stage_f + (32 * quad + lane) * kTPitch + 32 * kChunks * side;
@@ -457,14 +520,14 @@ __global__ void fp8_wait_selftest_kernel(int* status, long long limit_clocks) {
   if (!bar_wait_slow(smem_u32(&bar), 0, nullptr, limit_clocks)) f8_record_timeout(status);
 }
 
-template <typename Params>
+template <bool SEG, typename Params>
 cudaError_t launch_tile(const Params& p, int split, cudaStream_t st) {
   if (p.total_tiles == 0) return cudaSuccess;
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e =
-      f8_allow_smem(reinterpret_cast<const void*>(fp8_tile_kernel<Params>), tile_smem(kTMaxStages), ready);
+      f8_allow_smem(reinterpret_cast<const void*>(fp8_tile_kernel<Params, SEG>), tile_smem(kTMaxStages), ready);
   if (e != cudaSuccess) return e;
-  return f8_launch(fp8_tile_kernel<Params>, p, p.total_tiles * split, kTThreads, tile_smem(p.stages), split, st);
+  return f8_launch(fp8_tile_kernel<Params, SEG>, p, p.total_tiles * split, kTThreads, tile_smem(p.stages), split, st);
 }
 
 }  // namespace
@@ -474,11 +537,11 @@ cudaError_t launch_fp8_wait_selftest(int* status, long long limit_clocks, cudaSt
   return cudaGetLastError();
 }
 
-cudaError_t launch_fp8_gemm_tile(const F8GemmParamsN<kF8FewProducts>& p, int split, cudaStream_t st) {
-  return launch_tile(p, split, st);
+cudaError_t launch_fp8_gemm_tile(const F8GemmParamsN<kF8FewProducts>& p, int split, bool segments, cudaStream_t st) {
+  return segments ? launch_tile<true>(p, split, st) : launch_tile<false>(p, split, st);
 }
-cudaError_t launch_fp8_gemm_tile(const F8GemmParamsN<kMaxF8Products>& p, int split, cudaStream_t st) {
-  return launch_tile(p, split, st);
+cudaError_t launch_fp8_gemm_tile(const F8GemmParamsN<kMaxF8Products>& p, int split, bool segments, cudaStream_t st) {
+  return segments ? launch_tile<true>(p, split, st) : launch_tile<false>(p, split, st);
 }
 
 }  // namespace muon

@@ -291,6 +291,13 @@ ProductSize size_of(const muon_fp8_product& q) {
           (int32_t)(q.trans_a ? q.a.rows : q.a.cols)};
 }
 
+// A float32 result without an epilogue sums at most kF8SegmentBlocks k-blocks at a time on the
+// tensor cores, wherever it is computed (the others' own rounding is far larger).
+bool sums_in_parts(const muon_fp8_product& q) {
+  return q.d.data && q.d.dtype == MUON_F32 && q.epilogue == MUON_EPI_NONE;
+}
+bool long_sum(const muon_fp8_product& q) { return sums_in_parts(q) && blocks_of(size_of(q).k) > kF8SegmentBlocks; }
+
 // Products [b, end) of `live` in one launch: tiles of `tile` rows and columns.
 template <typename Params>
 muon_status fill_products(muon_handle* h, Params& p, const muon_fp8_product* products, const int* live, int count,
@@ -323,8 +330,7 @@ muon_status fill_products(muon_handle* h, Params& p, const muon_fp8_product* pro
     g.out_align = at % 32 == 0 ? 32 : at % 16 == 0 ? 16 : 0;
     if (q.c.data) g.c = kernel_dense(q.c);
     g.epi = (int32_t)q.epilogue;
-    // only a launch whose results are all float32 without an epilogue goes in segments
-    g.seg_kb = std::max<int32_t>(1, (int32_t)blocks_of(g.k));
+    g.seg_kb = long_sum(q) ? kF8SegmentBlocks : std::max<int32_t>(1, (int32_t)blocks_of(g.k));
     if (q.epilogue == MUON_EPI_RELU2_BACKWARD) {
       g.saved = kernel_fp8(q.saved);
       p.backward = 1;
@@ -349,9 +355,6 @@ muon_status launch_pair_products(muon_handle* h, const muon_fp8_product* product
   if (s) return s;
   for (int i = 0; i < count; ++i)
     if (p.p[i].epi == kF8EpiRelu2Backward && (s = encode_codes(h, &p.map_saved[i], products[live[i]].saved, 32))) return s;
-  bool segments = true;
-  for (int i = 0; i < count; ++i) segments = segments && p.p[i].out == kF8OutF32 && p.p[i].epi == kF8EpiNone;
-  for (int i = 0; i < count && segments; ++i) p.p[i].seg_kb = std::min(p.p[i].seg_kb, kF8SegmentBlocks);
   prof_begin(h, st, kFp8KindBase + MUON_FP8_KIND_MATMUL);
   const cudaError_t e = launch_fp8_gemm_pair(p, (int)std::min<int64_t>(tiles, h->sm_count / 2), st);
   prof_end(h, kFp8KindBase + MUON_FP8_KIND_MATMUL, st);
@@ -396,8 +399,14 @@ muon_status launch_tile_products(muon_handle* h, const muon_fp8_product* product
       fill_products(h, p, products, live, count, kFp8Block, &tiles, &min_kb);
   if (s) return s;
   p.stages = sh.stages;
+  bool segments = false;
+  for (int i = 0; i < count; ++i) {
+    const muon_fp8_product& q = products[live[i]];
+    const int64_t share = (blocks_of(size_of(q).k) + sh.split - 1) / sh.split;
+    segments = segments || (sums_in_parts(q) && share > kF8TileAccs * kF8SegmentBlocks);
+  }
   prof_begin(h, st, kFp8KindBase + MUON_FP8_KIND_MATMUL);
-  const cudaError_t e = launch_fp8_gemm_tile(p, sh.split, st);
+  const cudaError_t e = launch_fp8_gemm_tile(p, sh.split, segments, st);
   prof_end(h, kFp8KindBase + MUON_FP8_KIND_MATMUL, st);
   if (e != cudaSuccess) return cuda_fail(h, e, "8-bit product launch");
   h->last_launches++;
@@ -405,8 +414,8 @@ muon_status launch_tile_products(muon_handle* h, const muon_fp8_product* product
 }
 
 // The products products[live[..]], in launches of a few.
-muon_status launch_products(muon_handle* h, const muon_fp8_product* products, const std::vector<int>& live,
-                            cudaStream_t st) {
+muon_status launch_run(muon_handle* h, const muon_fp8_product* products, const std::vector<int>& live,
+                       cudaStream_t st) {
   for (size_t b = 0; b < live.size();) {
     int count = (int)std::min<size_t>(kMaxF8Products, live.size() - b);
     const int* items = live.data() + b;
@@ -428,6 +437,25 @@ muon_status launch_products(muon_handle* h, const muon_fp8_product* products, co
                               : launch_tile_products<kMaxF8Products>(h, products, items, count, sh, st);
     if (s) return s;
     b += (size_t)count;
+  }
+  return MUON_OK;
+}
+
+// All products of a call. Where there are more tiles than SMs, the kernels for them sum a
+// contraction in one accumulator or in segments, launch by launch, so long float32 sums go in
+// launches of their own (the items are independent; a CTA per tile has room for both kinds).
+muon_status launch_products(muon_handle* h, const muon_fp8_product* products, const std::vector<int>& live,
+                            cudaStream_t st) {
+  int64_t tiles = 0;
+  for (int i : live) {
+    const ProductSize z = size_of(products[i]);
+    tiles += blocks_of(z.m) * blocks_of(z.n);
+  }
+  std::vector<int> runs[2];
+  for (int i : live) runs[tiles > h->sm_count && long_sum(products[i]) ? 1 : 0].push_back(i);
+  for (const std::vector<int>& run : runs) {
+    const muon_status s = launch_run(h, products, run, st);
+    if (s) return s;
   }
   return MUON_OK;
 }
