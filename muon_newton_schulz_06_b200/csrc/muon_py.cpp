@@ -222,6 +222,9 @@ bool product(PyObject* p, muon_fp8_product* q, PyObject** first) {
   if (!truth(p, s_trans_a, &q->trans_a) || !truth(p, s_trans_b, &q->trans_b)) return false;
   if (is_instance(out.p, g_matrix) ? !fp8(out.p, "out", &q->d8) : !dense(out.p, "out", &q->d)) return false;
   if (add.p != Py_None && !dense(add.p, "add", &q->c)) return false;
+  // a tensor without entries has no address, which would say that there is no addend: any other one
+  // leaves its shape to the call's checks, which touch no memory of such a matrix
+  if (add.p != Py_None && q->c.data == nullptr) q->c.data = reinterpret_cast<void*>(static_cast<uintptr_t>(256));
   PyObject* code = PyDict_GetItemWithError(g_epilogues, epi.p);  // borrowed
   if (code == nullptr) {
     if (!PyErr_Occurred()) {
