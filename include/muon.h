@@ -231,8 +231,8 @@ MUON_API muon_status muon_newton_schulz_noalloc(const void* x_in, void* o_out, i
                                                 const float* coeffs, int ns_steps, float eps,
                                                 int* status, void* cuda_stream);
 
-/* Waits for the handle's last enqueued work and returns its device-side status
- * (MUON_OK or MUON_ERR_TIMEOUT), clearing it. */
+/* Waits for the work that the handle has enqueued (8-bit operators: on every stream) and
+ * returns its device-side status (MUON_OK or MUON_ERR_TIMEOUT), clearing it. */
 MUON_API muon_status muon_sync(muon_handle_t h);
 
 /* Diagnostic for the time-out path: enqueues on `cuda_stream` one kernel thread that
@@ -343,9 +343,9 @@ MUON_API muon_status muon_profile_read(muon_handle_t h, double* ms, int64_t* lau
  *    tensor are told apart when they share its pitch), except where stated.
  *  - No workspace and no allocation, after a small page-locked status word that a handle
  *    allocates with its first call (so MUON_DEBUG has no guard bands to check here).
- *    Calls may be captured into a CUDA graph (the first one too; the graph must not be
- *    replayed after muon_destroy), and calls on different streams may overlap on the GPU
- *    when their buffers allow it.  Results do not depend on timing: sums run in a fixed
+ *    Calls may be captured into a CUDA graph (the first one too; no replay of it may run, or
+ *    start, once muon_destroy is called), and calls on different streams may overlap on the
+ *    GPU when their buffers allow it: muon_sync and muon_destroy wait for all of them.  Results do not depend on timing: sums run in a fixed
  *    order.
  *  - The kernels use programmatic dependent launch: on one stream they still run one after
  *    another, as far as memory can tell.

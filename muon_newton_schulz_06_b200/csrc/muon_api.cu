@@ -1117,10 +1117,11 @@ namespace muon {
 // The 8-bit operators' status word (written by the device itself).
 static muon_status poll_fp8_status(muon_handle* h, bool wait) {
   if (!h->fp8_status) return MUON_OK;
-  if (wait && h->fp8_pending) {
-    const cudaError_t e = cudaEventSynchronize(h->fp8_event);
+  for (auto& m : h->fp8_marks) {
+    if (!wait || !m.pending) continue;
+    const cudaError_t e = cudaEventSynchronize(m.event);
     if (e != cudaSuccess) return cuda_fail(h, e, "fp8 event");
-    h->fp8_pending = false;
+    m.pending = false;
   }
   volatile int* word = h->fp8_status;
   if (*word != kDevOk) {
@@ -1133,7 +1134,10 @@ static muon_status poll_fp8_status(muon_handle* h, bool wait) {
 // Reports a device-side time-out of earlier work, if its status copy has landed.
 muon_status poll_status(muon_handle* h, bool wait) {
   const muon_status s8 = poll_fp8_status(h, wait);
-  if (s8 != MUON_OK) return s8;
+  if (s8 != MUON_OK) {
+    if (wait && h->status_pending) cudaEventSynchronize(h->status_event);  // its status is for the next call
+    return s8;
+  }
   if (!h->status_pending) return MUON_OK;
   cudaError_t e = wait ? cudaEventSynchronize(h->status_event) : cudaEventQuery(h->status_event);
   if (e == cudaErrorNotReady) {
@@ -1562,7 +1566,7 @@ muon_status muon_destroy(muon_handle_t h) {
     if (h->host_status) cudaFreeHost(h->host_status);
     if (h->status_event) cudaEventDestroy(h->status_event);
     if (h->fp8_status) cudaFreeHost(h->fp8_status);
-    if (h->fp8_event) cudaEventDestroy(h->fp8_event);
+    for (auto& m : h->fp8_marks) cudaEventDestroy(m.event);
 
     for (auto& p : h->ev_pending) {
       cudaEventDestroy(p.a);

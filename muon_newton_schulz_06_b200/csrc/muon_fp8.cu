@@ -140,7 +140,7 @@ F8Mat kernel_fp8(const muon_fp8_matrix& x) {
   return m;
 }
 
-// First call of a handle: the page-locked status word and the event.  Allowed while the
+// First call of a handle: the page-locked status word.  Allowed while the
 // stream is being captured (no work is enqueued), hence the relaxed capture mode.
 muon_status ensure_fp8(muon_handle* h) {
   if (h->fp8_status) return MUON_OK;
@@ -154,7 +154,6 @@ muon_status ensure_fp8(muon_handle* h) {
     e = cudaHostGetDevicePointer(&dev, word, 0);
     h->fp8_status_dev = static_cast<int*>(dev);
   }
-  if (e == cudaSuccess && !h->fp8_event) e = cudaEventCreateWithFlags(&h->fp8_event, cudaEventDisableTiming);
   cudaThreadExchangeStreamCaptureMode(&mode);
   if (e != cudaSuccess) {
     if (word) cudaFreeHost(word);
@@ -165,15 +164,48 @@ muon_status ensure_fp8(muon_handle* h) {
   return MUON_OK;
 }
 
-// Marks the end of a call's work for muon_sync (captured work has none to wait for).
-muon_status finish_fp8(muon_handle* h, cudaStream_t st) {
+// The mark for the end of this call's work on `st`, set up before anything is enqueued: that of the
+// stream's last call, or one whose work is over, or a new one.  -1 under capture (captured work has
+// none to wait for).
+muon_status take_mark(muon_handle* h, cudaStream_t st, int* mark) {
+  *mark = -1;
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
   cudaStreamIsCapturing(st, &cs);
   if (cs != cudaStreamCaptureStatusNone) return MUON_OK;
-  const cudaError_t e = cudaEventRecord(h->fp8_event, st);
-  if (e != cudaSuccess) return cuda_fail(h, e, "fp8 event");
-  h->fp8_pending = true;
+  unsigned long long id = 0;
+  cudaError_t e = cudaStreamGetId(st, &id);
+  if (e != cudaSuccess) return cuda_fail(h, e, "stream id");
+  for (size_t i = 0; i < h->fp8_marks.size(); ++i)
+    if (h->fp8_marks[i].stream == id) {
+      *mark = (int)i;
+      return MUON_OK;
+    }
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // another stream may be in a capture
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  for (size_t i = 0; i < h->fp8_marks.size() && *mark < 0; ++i)
+    if (!h->fp8_marks[i].pending || cudaEventQuery(h->fp8_marks[i].event) == cudaSuccess) *mark = (int)i;
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  cudaGetLastError();  // cudaErrorNotReady
+  if (*mark < 0) {
+    h->fp8_marks.reserve(h->fp8_marks.size() + 1);
+    cudaEvent_t event = nullptr;
+    if ((e = cudaEventCreateWithFlags(&event, cudaEventDisableTiming)) != cudaSuccess)
+      return cuda_fail(h, e, "fp8 event set-up");
+    *mark = (int)h->fp8_marks.size();
+    h->fp8_marks.push_back({id, event, false});
+  }
+  h->fp8_marks[*mark].stream = id;
+  h->fp8_marks[*mark].pending = false;
   return MUON_OK;
+}
+
+// Ends a call whose launches came to `s`: what was enqueued before an error is marked as well.
+muon_status finish_fp8(muon_handle* h, cudaStream_t st, int mark, muon_status s) {
+  if (mark < 0 || h->last_launches == 0) return s;
+  const cudaError_t e = cudaEventRecord(h->fp8_marks[mark].event, st);
+  if (e == cudaSuccess) h->fp8_marks[mark].pending = true;
+  else if (s == MUON_OK) return cuda_fail(h, e, "fp8 event");
+  return s;
 }
 
 struct NvtxScope {
@@ -218,15 +250,16 @@ muon_status run_passes(Call& call, int op, int kind, const std::vector<F8Pass>& 
                        cudaStream_t st) {
   muon_handle* h = call.h;
   muon_status s;
+  int mark;
   if ((s = call.check())) return s;
   if ((s = ensure_fp8(h))) return s;
   if ((s = poll_status(h, false))) return s;
+  if ((s = take_mark(h, st, &mark))) return s;
   h->last_launches = 0;
   const int relu2 = act == MUON_ACT_RELU2;
   s = passes.size() <= kF8FewPasses ? launch_passes<kF8FewPasses>(h, op, kind, passes, relu2, st)
                                     : launch_passes<kMaxF8Passes>(h, op, kind, passes, relu2, st);
-  if (s) return s;
-  return finish_fp8(h, st);
+  return finish_fp8(h, st, mark, s);
 }
 
 F8Pass make_pass(int64_t rows, int64_t cols) {
@@ -569,10 +602,12 @@ muon_status selftest_timeout(muon_handle_t h, int64_t limit_ns, void* cuda_strea
   if ((s = ensure_fp8(h))) return s;
   if ((s = poll_status(h, false))) return s;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  int mark;
+  if ((s = take_mark(h, st, &mark))) return s;
   const cudaError_t e = launch_fp8_wait_selftest(h->fp8_status_dev, 2 * limit_ns, st);
   if (e != cudaSuccess) return cuda_fail(h, e, "self-test launch");
   h->last_launches = 1;
-  return finish_fp8(h, st);
+  return finish_fp8(h, st, mark, MUON_OK);
 }
 
 muon_status matmul(muon_handle_t h, const muon_fp8_product* products, int n, void* cuda_stream) {
@@ -624,12 +659,13 @@ muon_status matmul(muon_handle_t h, const muon_fp8_product* products, int n, voi
     }
     if (!empty(m, nn)) live.push_back(i);
   }
+  int mark;
   if ((s = call.check())) return s;
   if ((s = ensure_fp8(h))) return s;
   if ((s = poll_status(h, false))) return s;
+  if ((s = take_mark(h, st, &mark))) return s;
   h->last_launches = 0;
-  if ((s = launch_products(h, products, live, st))) return s;
-  return finish_fp8(h, st);
+  return finish_fp8(h, st, mark, launch_products(h, products, live, st));
 }
 
 // No C++ exception (host memory that runs out) crosses the C boundary.

@@ -124,12 +124,17 @@ struct muon_handle {
   std::vector<const void*> checked_ptrs[2];
   int checked_next = 0;
   // 8-bit operators: their kernels record a time-out straight in this page-locked word
-  // (the device address is fp8_status_dev), so a call needs no copy to report one; the
-  // event marks the last call's end for muon_sync
+  // (the device address is fp8_status_dev), so a call needs no copy to report one
   int* fp8_status = nullptr;
   int* fp8_status_dev = nullptr;
-  cudaEvent_t fp8_event = nullptr;
-  bool fp8_pending = false;
+  // the end of the last call on each stream, for muon_sync and muon_destroy: these calls may
+  // overlap on several streams (known by their ids, which no later stream gets again)
+  struct Fp8Mark {
+    unsigned long long stream;
+    cudaEvent_t event;
+    bool pending;
+  };
+  std::vector<Fp8Mark> fp8_marks;
   double prof8_ms[MUON_FP8_KIND_COUNT] = {};
   int64_t prof8_launches[MUON_FP8_KIND_COUNT] = {};
 };

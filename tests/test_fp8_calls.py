@@ -5,9 +5,50 @@ import pytest
 import torch
 
 import muon_newton_schulz_06_b200 as mb
+from test_fp8_blocks import values
 from test_fp8_matmul import operands
 
 pytestmark = pytest.mark.gpu
+
+
+def slow_then_quick(opt):
+    """A wait of 0.2 s that runs out on one stream, then a call on another one."""
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    x, x8 = torch.ones(64, 64, device="cuda"), mb.Fp8Matrix(64, 64)
+    opt.fp8_quantize([x], [x8])
+    torch.cuda.synchronize()
+    mb.muon_selftest_fp8_timeout(opt.handle, 200_000_000, stream=a)
+    opt.fp8_quantize([x], [x8], stream=b)
+    return a, b, x, x8
+
+
+def test_sync_waits_for_every_stream():
+    opt = mb.Muon(0)
+    keep = slow_then_quick(opt)
+    try:
+        with pytest.raises(mb.MuonError) as ei:
+            mb.muon_sync(opt.handle)
+        assert ei.value.code == mb.MUON_ERR_TIMEOUT
+    finally:
+        torch.cuda.synchronize()
+    # many streams, used in turn, some of them gone
+    x, outs = keep[2], [mb.Fp8Matrix(64, 64) for _ in range(40)]
+    for o in outs:
+        opt.fp8_quantize([x], [o], stream=torch.cuda.Stream())
+    mb.muon_sync(opt.handle)
+    assert all((values(o) == 1).all() for o in outs)
+    opt.close()
+
+
+def test_destroy_waits_for_every_stream():
+    opt = mb.Muon(0)
+    keep = slow_then_quick(opt)
+    with pytest.raises(mb.MuonError) as ei:
+        mb.muon_destroy(opt.handle)
+    opt.handle = None
+    assert ei.value.code == mb.MUON_ERR_TIMEOUT
+    torch.cuda.synchronize()
+    del keep
 
 
 def test_addend_without_entries_is_refused():
