@@ -1131,15 +1131,29 @@ static muon_status poll_fp8_status(muon_handle* h, bool wait) {
   return MUON_OK;
 }
 
-// Reports a device-side time-out of earlier work, if its status copy has landed.
-muon_status poll_status(muon_handle* h, bool wait) {
+// Reports a device-side time-out of earlier work, if its status copy has landed.  While `st` is
+// being captured the step's status is left for a later call: the query is not allowed then.
+muon_status poll_status(muon_handle* h, bool wait, cudaStream_t st) {
   const muon_status s8 = poll_fp8_status(h, wait);
   if (s8 != MUON_OK) {
     if (wait && h->status_pending) cudaEventSynchronize(h->status_event);  // its status is for the next call
     return s8;
   }
   if (!h->status_pending) return MUON_OK;
-  cudaError_t e = wait ? cudaEventSynchronize(h->status_event) : cudaEventQuery(h->status_event);
+  cudaError_t e;
+  if (wait) {
+    e = cudaEventSynchronize(h->status_event);
+  } else {
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(st, &cs) != cudaSuccess || cs != cudaStreamCaptureStatusNone) {
+      cudaGetLastError();
+      return MUON_OK;
+    }
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // another stream may be in a capture
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    e = cudaEventQuery(h->status_event);
+    cudaThreadExchangeStreamCaptureMode(&mode);
+  }
   if (e == cudaErrorNotReady) {
     cudaGetLastError();
     return MUON_OK;
@@ -1194,7 +1208,7 @@ muon_status run_impl(muon_handle* h, const std::vector<CallMat>& cm, const int64
   if (!dg.ok) return fail(h, MUON_ERR_CUDA, "cannot select device %d", h->device);
   muon_status s = ensure_status(h);
   if (s) return s;
-  s = poll_status(h, false);
+  s = poll_status(h, false, st);
   if (s) return s;
   h->last_launches = 0;
   if (!plan_matches(h->plan, rows, cols, n, mode)) {
@@ -1440,7 +1454,7 @@ muon_status muon_selftest_wait_timeout(muon_handle_t h, int64_t limit_ns, void* 
   if (!dg.ok) return fail(h, MUON_ERR_CUDA, "cannot select device %d", h->device);
   muon_status s = ensure_status(h);
   if (s) return s;
-  if ((s = poll_status(h, false))) return s;
+  if ((s = poll_status(h, false, static_cast<cudaStream_t>(cuda_stream)))) return s;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   cudaError_t e = launch_wait_selftest(h->dev_status, (unsigned long long)limit_ns, st);
   if (e != cudaSuccess) return cuda_fail(h, e, "self-test launch");
@@ -1486,7 +1500,7 @@ muon_status muon_selftest_fail_next_alloc(muon_handle_t h) {
 muon_status muon_sync(muon_handle_t h) {
   if (!h) return MUON_ERR_INVALID_ARG;
   DeviceGuard dg(h->device);
-  return poll_status(h, true);
+  return poll_status(h, true, nullptr);
 }
 
 muon_status muon_profile_enable(muon_handle_t h, int enable) {
@@ -1560,7 +1574,7 @@ muon_status muon_destroy(muon_handle_t h) {
   muon_status s = MUON_OK;
   {
     DeviceGuard dg(h->device);
-    s = poll_status(h, true);
+    s = poll_status(h, true, nullptr);
     if (h->ws) cudaFree(h->ws);
     if (h->dev_status) cudaFree(h->dev_status);
     if (h->host_status) cudaFreeHost(h->host_status);

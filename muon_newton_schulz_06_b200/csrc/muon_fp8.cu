@@ -253,7 +253,7 @@ muon_status run_passes(Call& call, int op, int kind, const std::vector<F8Pass>& 
   int mark;
   if ((s = call.check())) return s;
   if ((s = ensure_fp8(h))) return s;
-  if ((s = poll_status(h, false))) return s;
+  if ((s = poll_status(h, false, st))) return s;
   if ((s = take_mark(h, st, &mark))) return s;
   h->last_launches = 0;
   const int relu2 = act == MUON_ACT_RELU2;
@@ -600,8 +600,8 @@ muon_status selftest_timeout(muon_handle_t h, int64_t limit_ns, void* cuda_strea
   if (!dg.ok) return fail(h, MUON_ERR_CUDA, "cannot select device %d", h->device);
   muon_status s;
   if ((s = ensure_fp8(h))) return s;
-  if ((s = poll_status(h, false))) return s;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  if ((s = poll_status(h, false, st))) return s;
   int mark;
   if ((s = take_mark(h, st, &mark))) return s;
   const cudaError_t e = launch_fp8_wait_selftest(h->fp8_status_dev, 2 * limit_ns, st);
@@ -662,7 +662,7 @@ muon_status matmul(muon_handle_t h, const muon_fp8_product* products, int n, voi
   int mark;
   if ((s = call.check())) return s;
   if ((s = ensure_fp8(h))) return s;
-  if ((s = poll_status(h, false))) return s;
+  if ((s = poll_status(h, false, st))) return s;
   if ((s = take_mark(h, st, &mark))) return s;
   h->last_launches = 0;
   return finish_fp8(h, st, mark, launch_products(h, products, live, st));

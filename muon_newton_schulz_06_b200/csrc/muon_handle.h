@@ -165,7 +165,7 @@ void prof_begin(muon_handle* h, cudaStream_t st, int kind);
 void prof_end(muon_handle* h, int kind, cudaStream_t st);
 
 // Reports a device-side time-out of earlier work that has become visible; with `wait`,
-// after that work has finished.
-muon_status poll_status(muon_handle* h, bool wait);
+// after that work has finished.  st: the stream of the call that asks.
+muon_status poll_status(muon_handle* h, bool wait, cudaStream_t st);
 
 }  // namespace muon

@@ -11,6 +11,71 @@ from test_fp8_matmul import operands
 pytestmark = pytest.mark.gpu
 
 
+def step_args(seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    w = [torch.randn(256, 384, generator=g, device="cuda").bfloat16()]
+    return w, [torch.randn(256, 384, generator=g, device="cuda").bfloat16()], [torch.zeros(256, 384, device="cuda")]
+
+
+def test_capture_after_an_optimizer_step():
+    """The step's status is still to be looked at when the capture begins."""
+    opt = mb.Muon(0)
+    w, g, m = step_args()
+    x8, w8, y = mb.Fp8Matrix(256, 384), mb.Fp8Matrix(256, 384), torch.zeros(256, 256, device="cuda")
+    opt.step(w, g, m, lr=0.02)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.fp8_quantize([g[0], w[0]], [x8, w8])
+        opt.fp8_matmul([mb.Fp8Product(x8, w8, y, trans_b=True)])
+    graph.replay()
+    torch.cuda.synchronize()
+    want = torch.from_numpy(values(x8)).cuda() @ torch.from_numpy(values(w8)).cuda().t()
+    assert (y.double() - want).abs().max() <= 1e-5 * want.abs().max()
+    mb.muon_sync(opt.handle)
+    del graph
+    opt.close()
+
+
+def test_step_captured_after_a_step():
+    w, g, m = step_args()
+    opt, ref = mb.Muon(0), mb.Muon(0)
+    rw, rm = [w[0].clone()], [m[0].clone()]
+    for _ in range(2):
+        ref.step(rw, g, rm, lr=0.02)
+    mb.muon_sync(ref.handle)
+    opt.step(w, g, m, lr=0.02)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.step(w, g, m, lr=0.02)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(w[0], rw[0]) and torch.equal(m[0], rm[0])
+    del graph
+    opt.close()
+    ref.close()
+
+
+def test_time_out_of_a_step_is_kept_through_a_capture():
+    opt = mb.Muon(0)
+    x8, x = mb.Fp8Matrix(64, 64), torch.ones(64, 64, device="cuda")
+    mb.muon_selftest_wait_timeout(opt.handle, 1_000_000)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.fp8_quantize([x], [x8])
+    with pytest.raises(mb.MuonError) as ei:
+        mb.muon_sync(opt.handle)
+    assert ei.value.code == mb.MUON_ERR_TIMEOUT
+    graph.replay()
+    mb.muon_sync(opt.handle)
+    torch.cuda.synchronize()
+    assert (values(x8) == 1).all()
+    del graph
+    opt.close()
+
+
 def slow_then_quick(opt):
     """A wait of 0.2 s that runs out on one stream, then a call on another one."""
     a, b = torch.cuda.Stream(), torch.cuda.Stream()
