@@ -15,6 +15,9 @@ namespace {
 
 constexpr int64_t kMaxDim8 = int64_t(1) << 24;
 constexpr int kMaxItems = 65535;
+// What one launch counts at most; a matrix above is refused before anything is enqueued.
+constexpr int64_t kMaxBlocks = INT32_MAX / 2;  // of a pass (up to two CTAs each)
+constexpr int64_t kMaxTiles = INT32_MAX / 8;   // of products (up to four CTAs each)
 
 int64_t blocks_of(int64_t n) { return (n + kFp8Block - 1) / kFp8Block; }
 bool empty(int64_t rows, int64_t cols) { return rows == 0 || cols == 0; }
@@ -228,13 +231,12 @@ muon_status launch_passes(muon_handle* h, int op, int kind, const std::vector<F8
     p.n = 0;
     for (; b < passes.size() && p.n < N; ++b) {
       const int64_t nb = blocks_of(passes[b].rows) * (int64_t)passes[b].blocks_c;
-      if (p.n > 0 && total + nb > INT32_MAX) break;
+      if (total + nb > kMaxBlocks) break;  // (one matrix always fits: run_passes)
       F8Pass& m = p.m[p.n++];
       m = passes[b];
       m.block_begin = (int32_t)total;
       total += nb;
     }
-    if (total > INT32_MAX) return fail(h, MUON_ERR_UNSUPPORTED, "a matrix has more than 2^31 - 1 blocks");
     p.total_blocks = (int)total;
     prof_begin(h, st, kFp8KindBase + kind);
     const cudaError_t e = launch_fp8_pass(op, p, st);
@@ -252,6 +254,9 @@ muon_status run_passes(Call& call, int op, int kind, const std::vector<F8Pass>& 
   muon_status s;
   int mark;
   if ((s = call.check())) return s;
+  for (const F8Pass& m : passes)
+    if (blocks_of(m.rows) * (int64_t)m.blocks_c > kMaxBlocks)
+      return fail(h, MUON_ERR_UNSUPPORTED, "a matrix of %d x %d has too many blocks", m.rows, m.cols);
   if ((s = ensure_fp8(h))) return s;
   if ((s = poll_status(h, false, st))) return s;
   if ((s = take_mark(h, st, &mark))) return s;
@@ -371,7 +376,6 @@ muon_status fill_products(muon_handle* h, Params& p, const muon_fp8_product* pro
     g.tile_begin = (int32_t)*total;
     *total += (int64_t)g.tiles_m * g.tiles_n;
     *min_kb = std::min(*min_kb, blocks_of(g.k));
-    if (*total > INT32_MAX / 8) return fail(h, MUON_ERR_UNSUPPORTED, "item %d: the result has too many tiles", live[i]);
     muon_status s;
     if (g.k > 0 && ((s = encode_codes(h, &p.map_a[p.n], q.a)) || (s = encode_codes(h, &p.map_b[p.n], q.b)))) return s;
     p.p[p.n++] = g;
@@ -461,8 +465,9 @@ muon_status launch_run(muon_handle* h, const muon_fp8_product* products, const s
         min_kb = std::min(min_kb, blocks_of(z.k));
       }
       sh = choose_shape(tiles, min_kb, h->sm_count);
-      if (!sh.persistent || count <= kF8PairProducts) break;
-      count = kF8PairProducts;
+      if (tiles > kMaxTiles) count = (count + 1) / 2;  // (one product always fits: matmul)
+      else if (sh.persistent && count > kF8PairProducts) count = kF8PairProducts;
+      else break;
     }
     const muon_status s = sh.persistent ? launch_pair_products(h, products, items, count, st)
                           : count <= kF8FewProducts
@@ -657,6 +662,8 @@ muon_status matmul(muon_handle_t h, const muon_fp8_product* products, int n, voi
                     (long long)q.saved.rows, (long long)q.saved.cols, (long long)m, (long long)nn);
       if ((s = call.fp8(q.saved, "saved", i, false))) return s;
     }
+    if (blocks_of(m) * blocks_of(nn) > kMaxTiles)
+      return fail(h, MUON_ERR_UNSUPPORTED, "item %d: the result has too many tiles", i);
     if (!empty(m, nn)) live.push_back(i);
   }
   int mark;

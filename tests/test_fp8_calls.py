@@ -116,6 +116,36 @@ def test_destroy_waits_for_every_stream():
     del keep
 
 
+def test_too_many_tiles_are_refused_before_the_first_launch():
+    """Sixteen products that fit one launch, then one whose result has more tiles than a launch can
+    count (a product of nothing: only its result has an address; it is never written)."""
+    h = mb.muon_init(0)
+    a, b, va, vb = operands(8, 16, 32, False, True, seed=1)
+    arena = torch.full((17, 8, 16), 7.0, device="cuda")
+    raw = (mb.muon_fp8_product * 17)()
+    for i in range(16):
+        raw[i].a, raw[i].b, raw[i].trans_b = a.c, b.c, 1
+        raw[i].d = mb.muon_dense(arena[i].data_ptr(), 8, 16, 16, mb.MUON_F32)
+    # the highest address of the call, so that its span holds no other buffer
+    rows, cols = 1 << 18, 1 << 24
+    top = max((t for t in (arena, torch.empty(1 << 20, device="cuda"), torch.empty(1 << 26, device="cuda"))),
+              key=lambda t: t.data_ptr())
+    raw[16].a.rows, raw[16].b.rows, raw[16].trans_b = rows, cols, 1
+    raw[16].d = mb.muon_dense(arena[16].data_ptr() if top is arena else top.data_ptr(), rows, cols, cols, mb.MUON_BF16)
+    if max(a.c.codes, b.c.codes, a.c.scales, b.c.scales) > raw[16].d.data:
+        pytest.skip("the operands lie above every other buffer")
+    lib = mb.load_library()
+    st = torch.cuda.current_stream().cuda_stream
+    assert lib.muon_fp8_matmul(h, raw, 17, st) == mb.MUON_ERR_UNSUPPORTED
+    assert b"tiles" in lib.muon_last_error(h)
+    torch.cuda.synchronize()
+    assert (arena == 7).all()
+    assert lib.muon_fp8_matmul(h, raw, 16, st) == mb.MUON_OK
+    want = (torch.from_numpy(va).cuda() @ torch.from_numpy(vb).cuda()).float()
+    assert all(torch.equal(arena[i], want) for i in range(16))
+    mb.muon_destroy(h)
+
+
 def test_addend_without_entries_is_refused():
     h = mb.muon_init(0)
     a, b, _, _ = operands(64, 96, 128, False, True)
