@@ -407,7 +407,8 @@ struct Shape {
   int stages = 6;           // and its ring
 };
 
-// tiles: 128 x 128 tiles of all products; min_kb: shortest contraction in blocks of 128.
+// tiles: 128 x 128 tiles of all products; min_kb, mean_kb: shortest contraction in blocks of 128,
+// and the mean over the tiles.
 // Times in a chain of calls on one B200:
 //   up to one tile per SM: a CTA per tile (64 x 512 x 512: 5.3 us, persistent 6.6; 1536 x 1536 x
 //   4096: 12.6, 16.2), its contraction split while the SMs hold all parts and each keeps 8
@@ -416,14 +417,16 @@ struct Shape {
 //   up to two per SM with short contractions: two CTAs per SM with half the ring (1536 x 2048 x
 //   512: 7.6, persistent 8.3; at 2048 x 2048 x 4096: 19.4, 17.3).
 //   more: persistent pairs (4096 x 4096 x 1024: 19.7, a CTA per tile 35).
-Shape choose_shape(int64_t tiles, int64_t min_kb, int sm_count) {
+//   Lists go by the mean over their tiles (1024 x 1024 x 128 beside 1280 x 1280 x 8192: pairs 26.5,
+//   two CTAs per SM 29.3; 1280 x 1280 x 4096: 17.3, 18.0).
+Shape choose_shape(int64_t tiles, int64_t min_kb, int64_t mean_kb, int sm_count) {
   Shape sh;
   if (tiles <= sm_count) {
     while (sh.split < 4 && tiles * sh.split * 2 <= sm_count && min_kb >= 16 * sh.split) sh.split *= 2;
     return sh;
   }
   sh.stages = 3;
-  sh.persistent = min_kb > 0 && (tiles > 2 * sm_count || min_kb >= 16);
+  sh.persistent = min_kb > 0 && (tiles > 2 * sm_count || mean_kb >= 16);  // (pairs need a sum to wait for)
   return sh;
 }
 
@@ -458,13 +461,15 @@ muon_status launch_run(muon_handle* h, const muon_fp8_product* products, const s
     const int* items = live.data() + b;
     Shape sh;
     while (true) {
-      int64_t tiles = 0, min_kb = INT64_MAX;
+      int64_t tiles = 0, min_kb = INT64_MAX, work = 0;
       for (int i = 0; i < count; ++i) {
         const ProductSize z = size_of(products[items[i]]);
-        tiles += blocks_of(z.m) * blocks_of(z.n);
-        min_kb = std::min(min_kb, blocks_of(z.k));
+        const int64_t t = blocks_of(z.m) * blocks_of(z.n), kb = blocks_of(z.k);
+        tiles += t;
+        min_kb = std::min(min_kb, kb);
+        work += t * kb;
       }
-      sh = choose_shape(tiles, min_kb, h->sm_count);
+      sh = choose_shape(tiles, min_kb, work / tiles, h->sm_count);
       if (tiles > kMaxTiles) count = (count + 1) / 2;  // (one product always fits: matmul)
       else if (sh.persistent && count > kF8PairProducts) count = kF8PairProducts;
       else break;
@@ -479,9 +484,12 @@ muon_status launch_run(muon_handle* h, const muon_fp8_product* products, const s
   return MUON_OK;
 }
 
-// All products of a call. Where there are more tiles than SMs, the kernels for them sum a
-// contraction in one accumulator or in segments, launch by launch, so long float32 sums go in
-// launches of their own (the items are independent; a CTA per tile has room for both kinds).
+// All products of a call (independent of one another, so in any order). Where there are more tiles
+// than SMs, the kernels for them sum a contraction in one accumulator or in segments, launch by
+// launch, so long float32 sums go in launches of their own; and so do products of nothing, which
+// the pairs do not take (128 x 256 x 0 beside 4096 x 4096 x 1024: 26.3 us, by a CTA per tile for
+// both 36.8; beside 2560 x 2304 x 640: 16.5, 15.4). Fewer tiles share a launch: a CTA per tile has
+// room for every kind.
 muon_status launch_products(muon_handle* h, const muon_fp8_product* products, const std::vector<int>& live,
                             cudaStream_t st) {
   int64_t tiles = 0;
@@ -489,8 +497,11 @@ muon_status launch_products(muon_handle* h, const muon_fp8_product* products, co
     const ProductSize z = size_of(products[i]);
     tiles += blocks_of(z.m) * blocks_of(z.n);
   }
-  std::vector<int> runs[2];
-  for (int i : live) runs[tiles > h->sm_count && long_sum(products[i]) ? 1 : 0].push_back(i);
+  std::vector<int> runs[3];
+  for (int i : live) {
+    const muon_fp8_product& q = products[i];
+    runs[tiles <= h->sm_count ? 0 : size_of(q).k == 0 ? 2 : long_sum(q) ? 1 : 0].push_back(i);
+  }
   for (const std::vector<int>& run : runs) {
     const muon_status s = launch_run(h, products, run, st);
     if (s) return s;

@@ -146,6 +146,38 @@ def test_too_many_tiles_are_refused_before_the_first_launch():
     mb.muon_destroy(h)
 
 
+def test_empty_contraction_beside_a_large_product():
+    """A weight gradient over no tokens in the list of a large one: a launch of its own, and the
+    large one keeps the launch that it has alone."""
+    h = mb.muon_init(0)
+    a, b, va, vb = operands(2560, 2304, 640, False, True, seed=2)
+    e, f = mb.Fp8Matrix(300, 0), mb.Fp8Matrix(200, 0)
+    d, alone = torch.empty(2560, 2304, device="cuda"), torch.empty(2560, 2304, device="cuda")
+    z, c = torch.full((300, 200), 3.0, device="cuda"), torch.randn(300, 200, device="cuda")
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(e, f, z, trans_b=True, add=c), mb.Fp8Product(a, b, d, trans_b=True)])
+    assert mb.muon_last_launch_count(h) == 2
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, alone, trans_b=True)])
+    assert mb.muon_last_launch_count(h) == 1
+    assert torch.equal(z, c) and torch.equal(d, alone)
+    assert torch.equal(d.double(), torch.from_numpy(va).cuda() @ torch.from_numpy(vb).cuda())
+    mb.muon_destroy(h)
+
+
+@pytest.mark.parametrize("K", [640, 1920, 2176, 8000])
+def test_short_contraction_beside_a_long_one(K):
+    """164 tiles of 128 x 128 whose mean contraction lies on either side of the rule between two CTAs
+    per SM and pairs."""
+    h = mb.muon_init(0)
+    a, b, va, vb = operands(1280, 1280, K, False, True, seed=K)
+    s, t, vs, vt = operands(1000, 1024, 100, True, False, seed=1)
+    d, e = (torch.empty(n, n2, device="cuda", dtype=torch.bfloat16) for n, n2 in ((1280, 1280), (1000, 1024)))
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(s, t, e, trans_a=True), mb.Fp8Product(a, b, d, trans_b=True)])
+    assert mb.muon_last_launch_count(h) == 1
+    for out, x, y in ((d, va, vb), (e, vs, vt)):
+        assert torch.equal(out, (torch.from_numpy(x).cuda() @ torch.from_numpy(y).cuda()).bfloat16())
+    mb.muon_destroy(h)
+
+
 def test_addend_without_entries_is_refused():
     h = mb.muon_init(0)
     a, b, _, _ = operands(64, 96, 128, False, True)
