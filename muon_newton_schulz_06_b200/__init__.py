@@ -409,6 +409,11 @@ class Fp8Matrix:
         bc = (self.cols + 127) // 128
         return ((self.rows + 127) // 128, bc) if self.blocks == "square" else (bc, self.rows)
 
+    def scales_count(self) -> int:
+        """Number of scale bytes."""
+        r, c = self._scale_shape()
+        return r * c
+
     @property
     def codes(self) -> torch.Tensor:
         if self._codes is None:
@@ -578,6 +583,28 @@ def muon_destroy(handle) -> None:
     _check(load_library().muon_destroy(handle))
 
 
+def _check_copies(copies, params):
+    """Refuses 8-bit copies that overlap one another or a parameter, as muon_fp8_quantize would
+    (column slices of one buffer lie beside each other)."""
+    spans = []                       # first byte, end, bytes per row, pitch, index: 3 i codes, scales, parameter
+    for i, (m, w) in enumerate(zip(copies, params)):
+        if m.rows and m.cols:
+            c, n, nw = m.c, m.scales_count(), w.numel() * w.element_size()
+            spans += [(c.codes, c.codes + (m.rows - 1) * c.ld + m.cols, m.cols, c.ld, 3 * i),
+                      (c.scales, c.scales + n, n, n, 3 * i + 1), (w.data_ptr(), w.data_ptr() + nw, nw, nw, 3 * i + 2)]
+    spans.sort()
+    for a in range(len(spans)):
+        lo, end, width, pitch, x = spans[a]
+        b = a + 1
+        while b < len(spans) and spans[b][0] < end:
+            lo2, _, width2, pitch2, y = spans[b]
+            off = (lo2 - lo) % pitch
+            if (x % 3 < 2 or y % 3 < 2) and not (pitch == pitch2 and off >= width and off + width2 <= pitch):
+                one, two = (("fp8_params[%d]", "the scales of fp8_params[%d]", "params[%d]")[k % 3] % (k // 3) for k in (x, y))
+                raise ValueError(f"{one} and {two} overlap")
+            b += 1
+
+
 class Muon:
     """Small convenience wrapper owning one handle."""
 
@@ -602,6 +629,7 @@ class Muon:
                     raise ValueError(f"fp8_params[{i}] needs 16-byte aligned rows")
             if len({m.c.codes for m in fp8_params if m.c.codes}) < sum(bool(m.c.codes) for m in fp8_params):
                 raise ValueError("fp8_params holds a matrix twice")
+            _check_copies(fp8_params, params)
         muon_step_ex(self.handle, params, grads, moms, **kw)
         if fp8_params is not None:
             muon_fp8_quantize(self.handle, params, fp8_params, stream=kw.get("stream"))

@@ -192,3 +192,35 @@ def test_addend_without_entries_is_refused():
     mb.muon_fp8_matmul(h, [mb.Fp8Product(mb.Fp8Matrix(0, 128), b, torch.empty(0, 96, device="cuda"), trans_b=True,
                                          add=torch.empty(0, 96, device="cuda"))])
     mb.muon_destroy(h)
+
+
+def test_step_refuses_copies_that_overlap_before_stepping():
+    opt = mb.Muon(0)
+    ws = [torch.ones(64, 64, device="cuda") for _ in range(2)]
+    gs, ms = [torch.ones_like(w) for w in ws], [torch.zeros_like(w) for w in ws]
+
+    def refused(copies, params=ws):
+        with pytest.raises(ValueError, match="overlap"):
+            opt.step(params, gs[:len(params)], ms[:len(params)], lr=0.1, fp8_params=copies)
+        torch.cuda.synchronize()
+        assert all((w == 1).all() for w in ws) and all((m == 0).all() for m in ms)
+
+    buf = torch.zeros(200, 64, dtype=torch.uint8, device="cuda")
+    sc = [torch.zeros(1, 1, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    part = [mb.Fp8Matrix(64, 64, codes=buf[o:o + 64], scales=s) for o, s in zip((0, 32), sc)]
+    refused(part)                                                             # codes
+    refused([mb.Fp8Matrix(64, 64, codes=buf[o:o + 64], scales=sc[0]) for o in (0, 64)])    # one scale for two
+    refused([mb.Fp8Matrix(64, 64, codes=buf[:64], scales=buf[2:3, :1])], ws[:1])            # scales in the codes
+    over = ws[0].view(-1).view(torch.uint8)[:64 * 64].view(64, 64)
+    refused([mb.Fp8Matrix(64, 64, codes=over, scales=sc[0])], ws[:1])         # over the weight
+    # column slices of one buffer lie beside each other
+    both = torch.zeros(64, 128, dtype=torch.uint8, device="cuda")
+    ok = [mb.Fp8Matrix(64, 64, codes=both[:, o:o + 64], scales=s) for o, s in zip((0, 64), sc)]
+    opt.step(ws, gs, ms, lr=0.1, fp8_params=ok)
+    mb.muon_sync(opt.handle)
+    ref = [mb.Fp8Matrix(64, 64) for _ in ws]
+    opt.fp8_quantize(ws, ref)
+    mb.muon_sync(opt.handle)
+    for o, r in zip(ok, ref):
+        assert torch.equal(o.codes, r.codes) and torch.equal(o.scales, r.scales)
+    opt.close()
