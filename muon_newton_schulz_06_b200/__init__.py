@@ -456,8 +456,8 @@ def _marshal():
         try:
             from . import _muon_py
         except ImportError as e:
-            raise RuntimeError("_muon_py.so is missing: build it with "
-                               "`python -m muon_newton_schulz_06_b200.build`") from e
+            raise RuntimeError(f"the marshalling module cannot be loaded ({e}): build it with "
+                               "`python -m muon_newton_schulz_06_b200.build` under this interpreter") from e
         addresses = tuple(ctypes.cast(f, ctypes.c_void_p).value for f in (
             lib.muon_fp8_quantize, lib.muon_fp8_dequantize, lib.muon_fp8_act_backward, lib.muon_fp8_matmul))
         _muon_py.setup(torch.Tensor, torch.bfloat16, torch.float32, Fp8Matrix, Fp8Product, _stream_ptr, FP8_EPILOGUES,

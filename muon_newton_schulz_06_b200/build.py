@@ -4,7 +4,8 @@
 
 nvcc compiles every kernel for sm_100a only (tcgen05 / TMA / TMEM instructions) and
 links the CUDA runtime statically, so the library needs no libcudart at load time.
-g++ compiles the binding's marshalling module _muon_py.so (CPython C API).
+g++ compiles the binding's marshalling module _muon_py (CPython C API) for the interpreter
+that runs the build; its file name carries that interpreter's tag.
 """
 import glob
 import os
@@ -16,7 +17,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmuon_b200.so")
 PY_SOURCE = os.path.join(HERE, "csrc", "muon_py.cpp")
-PY_LIB = os.path.join(HERE, "_muon_py.so")
+PY_LIB = os.path.join(HERE, "_muon_py" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -48,6 +49,9 @@ def build(verbose_ptxas=False, force=False):
                     "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"],
                     "-o", PY_LIB + ".tmp", PY_SOURCE], check=True)
     os.replace(PY_LIB + ".tmp", PY_LIB)
+    untagged = os.path.join(HERE, "_muon_py.so")      # of an earlier build: any interpreter would take it
+    if os.path.exists(untagged):
+        os.remove(untagged)
     return LIB
 
 
