@@ -590,16 +590,18 @@ def _check_copies(copies, params):
     for i, (m, w) in enumerate(zip(copies, params)):
         if m.rows and m.cols:
             c, n, nw = m.c, m.scales_count(), w.numel() * w.element_size()
-            spans += [(c.codes, c.codes + (m.rows - 1) * c.ld + m.cols, m.cols, c.ld, 3 * i),
-                      (c.scales, c.scales + n, n, n, 3 * i + 1), (w.data_ptr(), w.data_ptr() + nw, nw, nw, 3 * i + 2)]
+            spans += [(c.codes, c.codes + (m.rows - 1) * c.ld + m.cols, m.cols, c.ld if m.rows > 1 else 0, 3 * i),
+                      (c.scales, c.scales + n, n, 0, 3 * i + 1), (w.data_ptr(), w.data_ptr() + nw, nw, 0, 3 * i + 2)]
     spans.sort()
     for a in range(len(spans)):
         lo, end, width, pitch, x = spans[a]
         b = a + 1
         while b < len(spans) and spans[b][0] < end:
             lo2, _, width2, pitch2, y = spans[b]
-            off = (lo2 - lo) % pitch
-            if (x % 3 < 2 or y % 3 < 2) and not (pitch == pitch2 and off >= width and off + width2 <= pitch):
+            p = pitch or pitch2      # 0: a single row, which goes by the other's pitch
+            off = (lo2 - lo) % p if p else 0
+            apart = p > 0 and pitch2 in (0, p) and off >= width and off + width2 <= p
+            if (x % 3 < 2 or y % 3 < 2) and not apart:
                 one, two = (("fp8_params[%d]", "the scales of fp8_params[%d]", "params[%d]")[k % 3] % (k // 3) for k in (x, y))
                 raise ValueError(f"{one} and {two} overlap")
             b += 1

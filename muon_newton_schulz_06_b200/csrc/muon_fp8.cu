@@ -34,12 +34,15 @@ struct Span {
   uintptr_t hi() const { return lo + (uintptr_t)((rows - 1) * pitch + width); }
 };
 
-// Spans of one pitch that interleave without touching (column slices of one tensor).
+// Spans of one pitch that interleave without touching (column slices of one tensor). A single row
+// has the pitch of the other span.
 bool disjoint_columns(const Span& a, const Span& b) {
-  if (a.pitch != b.pitch || a.rows < 1 || b.rows < 1) return false;
-  const uint64_t d = (b.lo >= a.lo ? b.lo - a.lo : a.lo - b.lo) % (uint64_t)a.pitch;
-  const int64_t off = b.lo >= a.lo ? (int64_t)d : (d == 0 ? 0 : a.pitch - (int64_t)d);
-  return off >= a.width && off + b.width <= a.pitch;
+  if (a.rows < 1 || b.rows < 1 || (a.rows == 1 && b.rows == 1)) return false;
+  const int64_t pitch = a.rows == 1 ? b.pitch : a.pitch;
+  if (b.rows > 1 && b.pitch != pitch) return false;
+  const uint64_t d = (b.lo >= a.lo ? b.lo - a.lo : a.lo - b.lo) % (uint64_t)pitch;
+  const int64_t off = b.lo >= a.lo ? (int64_t)d : (d == 0 ? 0 : pitch - (int64_t)d);
+  return off >= a.width && off + b.width <= pitch;
 }
 
 struct Call {

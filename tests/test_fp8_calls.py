@@ -224,3 +224,30 @@ def test_step_refuses_copies_that_overlap_before_stepping():
     for o, r in zip(ok, ref):
         assert torch.equal(o.codes, r.codes) and torch.equal(o.scales, r.scales)
     opt.close()
+
+
+def test_single_rows_beside_column_slices():
+    """One row of a tensor lies beside other columns of all its rows, and scales in the padding
+    behind the codes."""
+    opt = mb.Muon(0)
+    big = torch.randn(20, 96, device="cuda")
+    m = mb.Fp8Matrix(20, 32)
+    one = mb.Fp8Matrix(1, 32)
+    opt.fp8_quantize([big[:, 32:64]], [m])
+    opt.fp8_quantize([big[7:8, 64:]], [one])
+    want, keep = (torch.from_numpy(values(x)).float().cuda() for x in (m, one)), big.clone()
+    opt.fp8_dequantize([m, one], [big[:, :32], big[7:8, 64:]])
+    mb.muon_sync(opt.handle)
+    keep[:, :32], keep[7:8, 64:] = want
+    assert torch.equal(big, keep)
+    with pytest.raises(mb.MuonError, match="overlap"):
+        opt.fp8_dequantize([m, one], [big[:, :32], big[7:8, 31:63]])
+    buf = torch.zeros(64, 80, dtype=torch.uint8, device="cuda")
+    packed = mb.Fp8Matrix(64, 64, codes=buf[:, :64], scales=buf[5:6, 64:65])
+    w, g, mo = torch.randn(64, 64, device="cuda"), torch.randn(64, 64, device="cuda"), torch.zeros(64, 64, device="cuda")
+    opt.step([w], [g], [mo], lr=0.1, fp8_params=[packed])
+    ref = mb.Fp8Matrix(64, 64)
+    opt.fp8_quantize([w], [ref])
+    mb.muon_sync(opt.handle)
+    assert torch.equal(packed.codes[:, :64], ref.codes) and torch.equal(packed.scales, ref.scales)
+    opt.close()
