@@ -524,19 +524,20 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       float sv_scale = 0.f;
       const float* table = slope;
       uint4 sv_next[2];
-      auto request_saved = [&](int c) {
+      auto request_saved = [&](auto plain, int c) {  // plain: see `finish`
         if (L::kHasSaved) return;
         const uint8_t* q = g.saved.codes + (int64_t)row * g.saved.ld + col0 + 32 * c;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int left = live ? g.n - (col0 + 32 * c + 16 * i) : 0;
-          sv_next[i] = left >= 16 ? *reinterpret_cast<const uint4*>(q + 16 * i)
-                       : left > 0 ? codes_edge(q + 16 * i, left)
-                                  : make_uint4(0u, 0u, 0u, 0u);
+          if (decltype(plain)::value || left <= 0 || left >= 16)
+            sv_next[i] = left > 0 ? *reinterpret_cast<const uint4*>(q + 16 * i) : make_uint4(0u, 0u, 0u, 0u);
+          else
+            sv_next[i] = codes_edge(q + 16 * i, left);
         }
       };
       if (backward) {
-        request_saved(rot);
+        request_saved(std::false_type(), rot);
         const uint32_t sb = live && col0 < g.n ? *f8_scale_at(g.saved, row, col0 / kFp8Block) : 127u;
         const int e = (int)sb - 127, parity = e & 1;
         sv_scale = sb == 255u ? __uint_as_float(0x7fc00000u) : f8_exp2((e - parity) / 2);
@@ -571,7 +572,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
           }
           const uint32_t w[8] = {sv_next[0].x, sv_next[0].y, sv_next[0].z, sv_next[0].w,
                                  sv_next[1].x, sv_next[1].y, sv_next[1].z, sv_next[1].w};
-          request_saved((c + 1) & 3);
+          request_saved(plain, (c + 1) & 3);
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             v[j] = __fmul_rn(__fmul_rn(table[(w[j >> 2] >> (8 * (j & 3))) & 255u], sv_scale), v[j]);
@@ -608,7 +609,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
           for (int k = 0; k < 4; ++k) {
             const int c = (k + rot) & 3;
             if (c >= chunks) {
-              if (backward) request_saved((c + 1) & 3);
+              if (backward) request_saved(plain, (c + 1) & 3);
               continue;
             }
             float v[32];
@@ -693,7 +694,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
         for (int k = 0; k < 4; ++k) {
           const int c = (k + rot) & 3;
           if (c >= chunks) {
-            if (backward && !codes_out) request_saved((c + 1) & 3);
+            if (backward && !codes_out) request_saved(plain, (c + 1) & 3);
             continue;
           }
           float v[32];
