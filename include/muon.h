@@ -297,7 +297,8 @@ MUON_API muon_status muon_selftest_fail_next_alloc(muon_handle_t h);
 /* Bytes of device workspace the handle currently holds. */
 MUON_API int64_t muon_workspace_bytes(muon_handle_t h);
 
-/* Number of kernel launches the last muon_step / muon_newton_schulz enqueued. */
+/* Number of kernel launches that the last call with launches enqueued (a step, a
+ * Newton-Schulz call, or an 8-bit operator's). */
 MUON_API int muon_last_launch_count(muon_handle_t h);
 
 /* Kernel kinds reported by muon_profile_read. */

@@ -13,6 +13,9 @@ import pytest
 import torch
 
 import muon_newton_schulz_06_b200 as mb
+from oracle import fp8
+from test_fp8_blocks import codes, exps, values
+from test_fp8_matmul import operands, roots
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +85,28 @@ def test_long_contraction_beside_a_short_one(h, short):
     mb.muon_fp8_matmul(h, [mb.Fp8Product(s, t, e, trans_a=True), mb.Fp8Product(a, b, d, trans_a=True)])
     check(d, va, vb)
     check(e, vs, vt)
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 257, 52000), (640, 1290, 40000), (1100, 1300, 13000)])
+def test_segments_beside_other_kinds_in_one_launch(h, M, N, K):
+    """Few tiles: a float32 contraction summed in segments, in rows of any alignment and in place,
+    beside 8-bit and bf16 results with their epilogues. Sums of small integers, exact in float32."""
+    a, b, va, vb = operands(M, N, K, True, False, seed=K)
+    want = torch.from_numpy(va).cuda() @ torch.from_numpy(vb).cuda()
+    assert want.abs().max() < 2 ** 19
+    s, t, vs, vt = operands(100, 120, 300, False, True, seed=1)
+    saved = roots(100, 120, "e4m3", "square", 2)
+    c = torch.randint(-9, 10, (M, N), device="cuda").float()
+    acc, big = c.clone(), torch.full((M, N + 7), 3.0, device="cuda")
+    q, g = mb.Fp8Matrix(100, 120), torch.empty(100, 120, device="cuda", dtype=torch.bfloat16)
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, acc, trans_a=True, add=acc),
+                           mb.Fp8Product(s, t, q, trans_b=True, epilogue="relu2"),
+                           mb.Fp8Product(s, t, g, trans_b=True, epilogue="relu2_backward", saved=saved)])
+    assert mb.muon_last_launch_count(h) == 1
+    assert torch.equal(acc.double(), want + c.double())
+    x, e = fp8.quantize(fp8.relu2(vs @ vt))
+    assert (codes(q) == x).all() and (exps(q) == e).all()
+    assert torch.equal(g.cpu(), torch.from_numpy(fp8.relu2_backward(vs @ vt, values(saved))).bfloat16())
+    mb.muon_fp8_matmul(h, [mb.Fp8Product(a, b, big[:, 3:3 + N], trans_a=True, add=c)])
+    assert torch.equal(big[:, 3:3 + N].double(), want + c.double())
+    assert (big[:, :3] == 3).all() and (big[:, 3 + N:] == 3).all()
