@@ -38,7 +38,7 @@
 // float32 result sums at most 4096 in tensor memory: a longer contraction goes tile by tile in
 // segments, which each epilogue thread adds up in 128 registers; the sum goes back to tensor
 // memory for the tile's end, so that nothing there needs the registers (6144 x 1536 x 16384:
-// 125 us; 144 us when each segment went through the result; bf16, without segments, 113-115 us).
+// 120-125 us; 144 us when each segment went through the result; bf16, without segments, 113-115 us).
 //
 // Every wait is bounded, the exchange of the maxima included.
 #include <type_traits>

@@ -77,12 +77,12 @@ def test_time_out_of_a_step_is_kept_through_a_capture():
 
 
 def slow_then_quick(opt):
-    """A wait of 0.2 s that runs out on one stream, then a call on another one."""
+    """A wait of half a second that runs out on one stream, then a call on another one."""
     a, b = torch.cuda.Stream(), torch.cuda.Stream()
     x, x8 = torch.ones(64, 64, device="cuda"), mb.Fp8Matrix(64, 64)
     opt.fp8_quantize([x], [x8])
     torch.cuda.synchronize()
-    mb.muon_selftest_fp8_timeout(opt.handle, 200_000_000, stream=a)
+    mb.muon_selftest_fp8_timeout(opt.handle, 500_000_000, stream=a)
     opt.fp8_quantize([x], [x8], stream=b)
     return a, b, x, x8
 
